@@ -219,6 +219,74 @@ sq_status fp8_block_mm(const uint8_t* q_a, const float* s_a, const uint8_t* q_w,
                        const float* s_w, void* y_bf16, int64_t M, int64_t N, int64_t K,
                        void* workspace, size_t ws_bytes, void* stream);
 
+/* Mixture-of-experts operators ------------------------------------------ */
+
+/* Residual addition + RMSNorm + SmoothQuant fold + dynamic INT8 quantisation.
+ * Per row m: residual_out = bf16_rne(f32(h) + f32(residual)) (one fp32 rounding,
+ * one to bf16), then sq_rmsnorm_quant's arithmetic on residual_out: scales per
+ * row (group == 0 or K: fp32 [M]) or per 128 columns (group == 128: fp32
+ * [M, K/128]).  h, residual, residual_out BF16 [M,K]; residual_out may be the
+ * residual or h itself (in place); one that overlaps them otherwise is refused
+ * (SQ_ERR_SHAPE).  inv_rms (fp32 [M], may be NULL) receives r.  eps > 0; K <= 24576.
+ * The factor 127 / amax is held at the largest finite fp32 (amax below about
+ * 3.7e-37).  A row that holds inf or NaN has unspecified codes and scales; the
+ * other rows are not affected.  The launch may overlap the tail of any
+ * preceding kernel (it reads and writes nothing before that kernel's end). */
+sq_status sq_add_rmsnorm_quant(const void* h_bf16, const void* residual_bf16, const float* gamma,
+                               float eps, int64_t group, void* residual_out_bf16, int8_t* q_i8,
+                               float* scales, float* inv_rms, int64_t M, int64_t K, void* stream);
+
+/* The same with OCP E4M3 codes and one scale per 128 columns (the arithmetic
+ * of sq_quant_fp8_per_group on the normalised row): q_e4m3 [M,K] bit patterns,
+ * s_a fp32 [M, K/128]. */
+sq_status sq_add_rmsnorm_quant_fp8(const void* h_bf16, const void* residual_bf16,
+                                   const float* gamma, float eps, void* residual_out_bf16,
+                                   uint8_t* q_e4m3, float* s_a, float* inv_rms, int64_t M,
+                                   int64_t K, void* stream);
+
+/* Gated activation + SmoothQuant fold + dynamic INT8 quantisation, between an
+ * expert's (or an MLP's) two products.  gate_up BF16 [T, 2K]: columns 0..K-1 are
+ * the gate g, K..2K-1 the other half u.  Per row: a = g / (1 + exp(-g)) * u in
+ * fp32 (within 2^-20 of the exact value, or 2^-40 |u| absolutely), v =
+ * a * inv_smooth[k] (inv_smooth fp32 [K], may be NULL: 1), then the codes and
+ * scales of sq_quant_per_token (group == 0 or K) or of sq_quant_per_group
+ * (group == 128) of v, with the factor 127 / amax held finite.  K % 128 == 0,
+ * K <= 24576.  Non-finite rows and the launch as for sq_add_rmsnorm_quant. */
+sq_status sq_silu_mul_quant(const void* gate_up_bf16, const float* inv_smooth, int64_t group,
+                            int8_t* q_i8, float* scales, int64_t T, int64_t K, void* stream);
+
+/* The same with OCP E4M3 codes and one scale per 128 columns. */
+sq_status sq_silu_mul_quant_fp8(const void* gate_up_bf16, const float* inv_smooth,
+                                uint8_t* q_e4m3, float* s_a, int64_t T, int64_t K, void* stream);
+
+/* W8A8 products grouped by expert, with ragged sizes.  Rows 0..T-1 are in the
+ * experts' order: expert e owns rows offsets[e] .. offsets[e+1] - 1 (offsets
+ * int32 [E+1] on the device, non-decreasing, 0 <= offsets[e] <= T; a group may
+ * be empty) and row t reads token rows[t] of q_a (rows int32 [T] on the device;
+ * NULL: token t, and then M == T).  For a row t of expert e, with m = rows[t]:
+ *   acc[n] = sum_k q_a[m,k] * q_w[e,n,k] (exact int32),
+ *   y[t,n] = bf16_rne((f32(acc) * s_tok[m]) * s_ch[e,n]).
+ * q_a int8 [M,K], s_tok fp32 [M], q_w int8 [E,N,K], s_ch fp32 [E,N], y BF16
+ * [T,N].  A rows[t] outside [0, M) is a padding row: y[t,:] = 0.  Rows before
+ * offsets[0] and from offsets[E] on are left as they were.  Offsets outside
+ * [0, T] or decreasing are held to the range and to the largest before them, so
+ * they reach no memory outside the buffers.  E <= 1024, N % 16 == 0, K % 128 ==
+ * 0; T == 0 is a no-op.  Needs no workspace.  The launch may overlap the tail of
+ * any preceding kernel (it reads and writes nothing before that kernel's end). */
+sq_status w8a8_grouped_mm(const int8_t* q_a, const float* s_tok, const int32_t* rows,
+                          const int8_t* q_w, const float* s_ch, const int32_t* offsets,
+                          void* y_bf16, int64_t T, int64_t M, int64_t E, int64_t N, int64_t K,
+                          void* stream);
+
+/* FP8 block-scaled products grouped by expert: rows and offsets as above, the
+ * arithmetic of fp8_block_mm.  q_a E4M3 [M,K], s_a fp32 [M, K/128], q_w E4M3
+ * [E,N,K], s_w fp32 [E, N/128, K/128] (sq_quant_fp8_block of each expert's
+ * weights); N % 128 == 0. */
+sq_status fp8_block_grouped_mm(const uint8_t* q_a, const float* s_a, const int32_t* rows,
+                               const uint8_t* q_w, const float* s_w, const int32_t* offsets,
+                               void* y_bf16, int64_t T, int64_t M, int64_t E, int64_t N, int64_t K,
+                               void* stream);
+
 /* Bytes of workspace an operation needs for these sizes (0 = none). */
 size_t sq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K);
 

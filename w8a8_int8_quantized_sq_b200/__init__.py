@@ -22,6 +22,15 @@ Functions (CUDA tensors in, CUDA tensors out, on the current stream):
   quant_fp8_per_group(x, inv_s)        -> (q e4m3 uint8 [M,K], s_a f32 [M,K/128])
   quant_fp8_block(w, smooth)           -> (q e4m3 uint8 [N,K], s_w f32 [N/128,K/128])
   fp8_block_mm(q_a, s_a, q_w, s_w)     -> y bf16 [M,N]
+Mixture-of-experts operators (rows sorted by expert, offsets int32 [E+1]):
+  add_rmsnorm_quant(h, residual, gamma, eps, group)
+                                       -> (residual' bf16 [M,K], q int8 [M,K], scales, inv_rms)
+  add_rmsnorm_quant_fp8(h, residual, gamma, eps)
+                                       -> (residual', q e4m3 uint8 [M,K], s_a, inv_rms)
+  w8a8_grouped_mm(q_a, s_tok, q_w, s_ch, offsets, rows) -> y bf16 [T,N]
+  silu_mul_quant(gate_up, inv_s, group) -> (q int8 [T,K], scales)
+  silu_mul_quant_fp8(gate_up, inv_s)   -> (q e4m3 uint8 [T,K], s_a)
+  fp8_block_grouped_mm(q_a, s_a, q_w, s_w, offsets, rows) -> y bf16 [T,N]
 """
 from __future__ import annotations
 
@@ -84,6 +93,14 @@ def lib() -> ctypes.CDLL:
                 "sq_quant_fp8_per_group": [vp, vp, vp, vp, i64, i64, vp],
                 "sq_quant_fp8_block": [vp, vp, vp, vp, i64, i64, vp],
                 "fp8_block_mm": [vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp],
+                "sq_add_rmsnorm_quant": [vp, vp, vp, ctypes.c_float, i64, vp, vp, vp, vp, i64, i64,
+                                         vp],
+                "sq_add_rmsnorm_quant_fp8": [vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, i64, i64,
+                                             vp],
+                "sq_silu_mul_quant": [vp, vp, i64, vp, vp, i64, i64, vp],
+                "sq_silu_mul_quant_fp8": [vp, vp, vp, vp, i64, i64, vp],
+                "w8a8_grouped_mm": [vp] * 7 + [i64] * 5 + [vp],
+                "fp8_block_grouped_mm": [vp] * 7 + [i64] * 5 + [vp],
                 "sq_mma_peak": [ctypes.c_int, ctypes.c_int, vp, vp],
                 "sq_selftest_wait_timeout": [i64, vp, vp],
             }
@@ -105,7 +122,9 @@ EXPORTS = ("sq_quant_per_token", "w8a8_scaled_mm", "w8a8_gs128_mm", "w8a16_mm",
            "sq_w8a8_linear", "sq_set_overlap", "sq_describe_plan", "sq_fold_norm_weight",
            "sq_rmsnorm_quant", "sq_quant_per_group", "w8a8_pg128_mm", "w8a16_group_mm",
            "sq_quant_fp8_per_group", "sq_quant_fp8_block", "fp8_block_mm", "sq_mma_peak",
-           "sq_selftest_wait_timeout")
+           "sq_selftest_wait_timeout", "sq_add_rmsnorm_quant", "sq_add_rmsnorm_quant_fp8",
+           "sq_silu_mul_quant", "sq_silu_mul_quant_fp8", "w8a8_grouped_mm",
+           "fp8_block_grouped_mm")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -333,6 +352,130 @@ def fp8_block_mm(q_a, s_a, q_w, s_w):
         _ptr(q_a), _ptr(s_a), _ptr(q_w), _ptr(s_w), _ptr(y), M, N, K, _ptr(ws), wsb,
         _stream(q_a.device)))
     return y
+
+
+# ---- mixture-of-experts operators.  Tensors may be on any device: the launch goes
+# to theirs, on that device's current stream.
+
+def _args(fn: str, device, *wanted) -> list:
+    """Addresses of `wanted` = (name, tensor or None, dtype, shape) after checking each."""
+    got = []
+    for name, t, dtype, shape in wanted:
+        if t is None:
+            got.append(None)
+            continue
+        if t.device != device or not t.is_cuda:
+            raise ValueError(f"{fn}: {name} is on {t.device}, expected {device} (a CUDA device)")
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is {t.dtype} {list(t.shape)}, expected contiguous "
+                             f"{dtype} {list(shape)}")
+        got.append(t.data_ptr())
+    return got
+
+
+def _launch(fn: str, device, *args) -> None:
+    """Call the C entry point on the device's current stream, with it as the current device."""
+    f = getattr(lib(), fn)
+    if device.index == torch._C._cuda_getDevice():
+        _check(fn, f(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+        return
+    with torch.cuda.device(device):
+        _check(fn, f(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+
+
+def _matrix(fn: str, name: str, t: torch.Tensor, dims: int = 2) -> None:
+    if t.dim() != dims or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor of {dims} dimensions")
+
+
+def _add_rmsnorm(fn, h, residual, gamma, eps, group, residual_out, code):
+    _matrix(fn, "h", h)
+    M, K = h.shape
+    dev, bf16, f32 = h.device, torch.bfloat16, torch.float32
+    per_row = code == torch.int8 and group != 128
+    if residual_out is None:
+        residual_out = torch.empty_like(h)
+    q = torch.empty((M, K), dtype=code, device=dev)
+    sc = torch.empty((M,) if per_row else (M, K // 128), dtype=f32, device=dev)
+    r = torch.empty((M,), dtype=f32, device=dev)
+    ph, pr, pg, po = _args(fn, dev, ("h", h, bf16, (M, K)), ("residual", residual, bf16, (M, K)),
+                           ("gamma", gamma, f32, (K,)),
+                           ("residual_out", residual_out, bf16, (M, K)))
+    mode = () if code == torch.uint8 else (group,)
+    _launch(fn, dev, ph, pr, pg, eps, *mode, po, q.data_ptr(), sc.data_ptr(), r.data_ptr(), M, K)
+    return residual_out, q, sc, r
+
+
+def add_rmsnorm_quant(h, residual, gamma, eps: float, group: int = 0,
+                      residual_out: Optional[torch.Tensor] = None):
+    """residual' = h + residual (bf16), then RMSNorm + fold + INT8 quantisation of it:
+    (residual', q, scales, inv_rms); group 0 = one scale per token, 128 = one per 128
+    columns.  residual_out may be `residual` or `h` (in place)."""
+    return _add_rmsnorm("sq_add_rmsnorm_quant", h, residual, gamma, eps, group, residual_out,
+                        torch.int8)
+
+
+def add_rmsnorm_quant_fp8(h, residual, gamma, eps: float,
+                          residual_out: Optional[torch.Tensor] = None):
+    """The same with E4M3 codes (uint8 bit patterns) and scales [M, K/128]."""
+    return _add_rmsnorm("sq_add_rmsnorm_quant_fp8", h, residual, gamma, eps, 128, residual_out,
+                        torch.uint8)
+
+
+def _silu_mul(fn, gate_up, inv_s, group, code):
+    _matrix(fn, "gate_up", gate_up)
+    T, K = gate_up.shape[0], gate_up.shape[1] // 2
+    dev, f32 = gate_up.device, torch.float32
+    per_row = code == torch.int8 and group != 128
+    q = torch.empty((T, K), dtype=code, device=dev)
+    sc = torch.empty((T,) if per_row else (T, K // 128), dtype=f32, device=dev)
+    pg, ps = _args(fn, dev, ("gate_up", gate_up, torch.bfloat16, (T, 2 * K)),
+                   ("inv_s", inv_s, f32, (K,)))
+    mode = () if code == torch.uint8 else (group,)
+    _launch(fn, dev, pg, ps, *mode, q.data_ptr(), sc.data_ptr(), T, K)
+    return q, sc
+
+
+def silu_mul_quant(gate_up, inv_s: Optional[torch.Tensor] = None, group: int = 0):
+    """silu(gate) * up * inv_s of gate_up [T, 2K], INT8 quantised: (q, scales)."""
+    return _silu_mul("sq_silu_mul_quant", gate_up, inv_s, group, torch.int8)
+
+
+def silu_mul_quant_fp8(gate_up, inv_s: Optional[torch.Tensor] = None):
+    """The same with E4M3 codes (uint8 bit patterns) and scales [T, K/128]."""
+    return _silu_mul("sq_silu_mul_quant_fp8", gate_up, inv_s, 128, torch.uint8)
+
+
+def _grouped(fn, q_a, s_a, q_w, s_w, offsets, rows, out, code):
+    _matrix(fn, "q_a", q_a)
+    _matrix(fn, "q_w", q_w, 3)
+    M, K = q_a.shape
+    E, N = q_w.shape[0], q_w.shape[1]
+    T = M if rows is None else rows.numel()
+    dev, f32, i32 = q_a.device, torch.float32, torch.int32
+    y = torch.empty((T, N), dtype=torch.bfloat16, device=dev) if out is None else out
+    i8 = code == torch.int8
+    pa, psa, pr, pw, psw, po, py = _args(
+        fn, dev, ("q_a", q_a, code, (M, K)), ("s_a", s_a, f32, (M,) if i8 else (M, K // 128)),
+        ("rows", rows, i32, (T,)), ("q_w", q_w, code, (E, N, K)),
+        ("s_w", s_w, f32, (E, N) if i8 else (E, N // 128, K // 128)),
+        ("offsets", offsets, i32, (E + 1,)), ("out", y, torch.bfloat16, (T, N)))
+    _launch(fn, dev, pa, psa, pr, pw, psw, po, py, T, M, E, N, K)
+    return y
+
+
+def w8a8_grouped_mm(q_a, s_tok, q_w, s_ch, offsets, rows: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None):
+    """W8A8 products grouped by expert: row t (of expert e, offsets[e] <= t <
+    offsets[e+1]) multiplies token rows[t] (None: token t) by q_w[e].  Rows outside the
+    groups are left as they were in `out` (unspecified without it)."""
+    return _grouped("w8a8_grouped_mm", q_a, s_tok, q_w, s_ch, offsets, rows, out, torch.int8)
+
+
+def fp8_block_grouped_mm(q_a, s_a, q_w, s_w, offsets, rows: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None):
+    """FP8 block-scaled products grouped by expert, rows as in w8a8_grouped_mm."""
+    return _grouped("fp8_block_grouped_mm", q_a, s_a, q_w, s_w, offsets, rows, out, torch.uint8)
 
 
 class PlanInfo(ctypes.Structure):

@@ -1,0 +1,199 @@
+// rowquant.cuh -- HBM-bound kernels that fuse a row operation with 8-bit
+// quantisation: residual addition + RMSNorm, and the gated activation
+// silu(gate) * up.  Codes are INT8 with one scale per row or per 128 columns, or
+// E4M3 with one scale per 128 columns (the arithmetic of quant.cuh).
+//
+// One pass over HBM: TPR threads own a row and hold it in registers (NV vectors
+// of 8 columns per thread) from the loads to the codes, so nothing is read
+// twice and no shared memory but the reduction slots is touched.
+#pragma once
+#include "quant.cuh"
+
+namespace sq {
+
+enum : int { RQ_ADD_NORM = 0, RQ_SILU = 1 };           // row operation
+enum : int { RQ_I8_ROW = 0, RQ_I8_GROUP = 1, RQ_E4M3_GROUP = 2 };  // output format
+
+struct RowQuantArgs {
+  const __nv_bfloat16* a;   // h [M, K], or gate_up [M, 2 K]
+  const __nv_bfloat16* b;   // residual [M, K] (may be b_out)
+  __nv_bfloat16* b_out;     // residual' [M, K]
+  const float* vec;         // gamma [K], or 1/s [K] (may be NULL)
+  uint8_t* q;               // codes [M, K]
+  float* scales;            // [M] or [M, K / 128]
+  float* r_out;             // 1/rms [M] or NULL
+  int64_t M;
+  int K;
+  float eps;
+};
+
+// silu(g) * u = g / (1 + exp(-g)) * u.  The exponential and the quotient are the
+// hardware approximations: together within 2^-20 of the value for |g| <= 32, far
+// below half a step of the 8-bit code that follows; beyond, 1 + exp(-g) is 1 or
+// the value is below 2^-40 |u|.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
+}
+
+template <int TPR, int NV, int OP, int FMT>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+    row_quant_kernel(const RowQuantArgs p) {
+  constexpr int BLOCK = TPR < 128 ? 128 : TPR;
+  constexpr int RPB = BLOCK / TPR;     // rows per block
+  constexpr int NW = TPR / 32;         // warps per row
+  constexpr bool GROUP = FMT != RQ_I8_ROW;
+  constexpr bool FP8 = FMT == RQ_E4M3_GROUP;
+  constexpr float QMAX = FP8 ? 448.0f : 127.0f;
+  // two slots, taken in turn: a row's sums are read while the next row's are written
+  __shared__ double red_d[2][RPB][NW];
+  __shared__ float red[2][RPB][NW];
+  const int rib = threadIdx.x / TPR;
+  const int t = threadIdx.x % TPR;
+  const int lane = threadIdx.x & 31;
+  const int wig = t >> 5;
+  const int K = p.K;
+  griddep_launch_dependents();
+  griddep_wait();  // nothing above touches global memory: the launch may overlap any kernel
+
+  int slot = 0;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * RPB; row0 < p.M;
+       row0 += static_cast<int64_t>(gridDim.x) * RPB, slot ^= 1) {
+    const int64_t row = row0 + rib;
+    const bool active = row < p.M;
+    float v[NV][8];
+    // ---- the row, in fp32 registers
+    if constexpr (OP == RQ_ADD_NORM) {
+      uint4 x[NV], y[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + t) * 8;
+        x[j] = y[j] = make_uint4(0, 0, 0, 0);
+        if (active && c < K) {
+          x[j] = *reinterpret_cast<const uint4*>(p.a + row * K + c);
+          y[j] = *reinterpret_cast<const uint4*>(p.b + row * K + c);
+        }
+      }
+      double ss = 0.0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + t) * 8;
+        float f[8];
+        bf16x8_to_f32(x[j], v[j]);
+        bf16x8_to_f32(y[j], f);
+        uint32_t s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // the sum is kept in bf16: what is stored is what is normalised
+          s[i] = pack_bf16x2(__fadd_rn(v[j][2 * i], f[2 * i]), __fadd_rn(v[j][2 * i + 1], f[2 * i + 1]));
+        const uint4 sum = make_uint4(s[0], s[1], s[2], s[3]);
+        if (active && c < K) *reinterpret_cast<uint4*>(p.b_out + row * K + c) = sum;
+        bf16x8_to_f32(sum, v[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const double d = static_cast<double>(v[j][i]);
+          ss = __fma_rn(d, d, ss);
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if constexpr (NW > 1) {
+        if (lane == 0) red_d[slot][rib][wig] = ss;
+        __syncthreads();
+        ss = 0.0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) ss += red_d[slot][rib][w];
+      }
+      const float ms = __fdiv_rn(__double2float_rn(ss), static_cast<float>(K));
+      const float rn = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
+      if (active && p.r_out && t == 0) p.r_out[row] = rn;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + t) * 8;
+        if (c < K) {
+          const float4 g0 = __ldg(reinterpret_cast<const float4*>(p.vec + c));
+          const float4 g1 = __ldg(reinterpret_cast<const float4*>(p.vec + c) + 1);
+          const float gm[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[j][i] = __fmul_rn(__fmul_rn(v[j][i], rn), gm[i]);
+        }
+      }
+    } else {
+      uint4 x[NV], y[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + t) * 8;
+        x[j] = y[j] = make_uint4(0, 0, 0, 0);
+        if (active && c < K) {
+          x[j] = __ldg(reinterpret_cast<const uint4*>(p.a + row * 2 * K + c));
+          y[j] = __ldg(reinterpret_cast<const uint4*>(p.a + row * 2 * K + K + c));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + t) * 8;
+        float u[8];
+        bf16x8_to_f32(x[j], v[j]);
+        bf16x8_to_f32(y[j], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = silu_mul(v[j][i], u[i]);
+        if (p.vec && c < K) {
+          const float4 g0 = __ldg(reinterpret_cast<const float4*>(p.vec + c));
+          const float4 g1 = __ldg(reinterpret_cast<const float4*>(p.vec + c) + 1);
+          const float gm[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[j][i] = __fmul_rn(v[j][i], gm[i]);
+        }
+      }
+    }
+    // ---- largest magnitude: of the row, or of each 128 columns (16 adjacent lanes)
+    float amax = 0.0f, gmax[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
+      if constexpr (GROUP) {
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      }
+      gmax[j] = m;
+      amax = fmaxf(amax, m);
+    }
+    if constexpr (!GROUP) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      if constexpr (NW > 1) {
+        if (lane == 0) red[slot][rib][wig] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) amax = fmaxf(amax, red[slot][rib][w]);
+      }
+      if (active && t == 0) p.scales[row] = __fdiv_rn(amax, QMAX);
+    }
+    // ---- codes
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + t) * 8;
+      const float am = GROUP ? gmax[j] : amax;
+      // held finite: a largest magnitude below 2^-119 would make it infinite, and zeros NaN
+      const float mult = am > 0.0f ? fminf(__fdiv_rn(QMAX, am), 3.402823466e38f) : 0.0f;
+      if (!active || c >= K) continue;
+      if (GROUP && (t & 15) == 0) p.scales[row * (K >> 7) + (c >> 7)] = __fdiv_rn(am, QMAX);
+      uint32_t pk[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* f = &v[j][4 * i];
+        if constexpr (FP8) {
+          const uint32_t lo = e4m3x2_bits(__fmul_rn(f[0], mult), __fmul_rn(f[1], mult));
+          const uint32_t hi = e4m3x2_bits(__fmul_rn(f[2], mult), __fmul_rn(f[3], mult));
+          pk[i] = am > 0.0f ? (lo | (hi << 16)) : 0u;  // an all-zero group: zero codes
+        } else {
+          pk[i] = pack_code_bytes(quant_byte_bits(f[0], mult), quant_byte_bits(f[1], mult),
+                                  quant_byte_bits(f[2], mult), quant_byte_bits(f[3], mult));
+        }
+      }
+      *reinterpret_cast<uint2*>(p.q + row * K + c) = make_uint2(pk[0], pk[1]);
+    }
+  }
+}
+
+}  // namespace sq

@@ -11,8 +11,10 @@
 #include "gemm2.cuh"
 #include "gemm3.cuh"
 #include "gemv.cuh"
+#include "grouped.cuh"
 #include "peak.cuh"
 #include "quant.cuh"
+#include "rowquant.cuh"
 
 using namespace sq;
 
@@ -648,6 +650,215 @@ sq_status quant_rows(const void* x, const float* vec, int8_t* q, float* scales, 
              : launch_quant<256, false>(x, vec, q, scales, nseg, K, group, st);
 }
 
+// Launch with the programmatic-dependent attribute: the kernel may be set up
+// while the preceding kernel on the stream still runs.  Only for kernels that
+// touch no global memory before griddep_wait.
+template <class... P, class... A>
+sq_status launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem,
+                           cudaStream_t st, int cluster, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return SQ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+template <int TPR, int NV, int OP, int FMT>
+sq_status launch_row_quant(const RowQuantArgs& a, cudaStream_t st) {
+  constexpr int block = TPR < 128 ? 128 : TPR;
+  constexpr int rpb = block / TPR;
+  int64_t blocks = (a.M + rpb - 1) / rpb;
+  if (blocks > 1 << 20) blocks = 1 << 20;
+  return launch_dependent(row_quant_kernel<TPR, NV, OP, FMT>, static_cast<unsigned>(blocks), block,
+                          0, st, 1, a);
+}
+
+// Threads per row: the fewest that hold the row in at most four (512 threads:
+// six) vectors of eight columns each.
+template <int OP, int FMT>
+sq_status row_quant(const RowQuantArgs& a, cudaStream_t st) {
+  const int vec = a.K / 8;
+  if (vec <= 32 * 4) {
+    switch ((vec + 31) / 32) {
+      case 1: return launch_row_quant<32, 1, OP, FMT>(a, st);
+      case 2: return launch_row_quant<32, 2, OP, FMT>(a, st);
+      case 3: return launch_row_quant<32, 3, OP, FMT>(a, st);
+      default: return launch_row_quant<32, 4, OP, FMT>(a, st);
+    }
+  }
+  if (vec <= 128 * 4) {
+    switch ((vec + 127) / 128) {
+      case 2: return launch_row_quant<128, 2, OP, FMT>(a, st);
+      case 3: return launch_row_quant<128, 3, OP, FMT>(a, st);
+      default: return launch_row_quant<128, 4, OP, FMT>(a, st);
+    }
+  }
+  if (vec <= 256 * 4) {
+    if (vec <= 256 * 3) return launch_row_quant<256, 3, OP, FMT>(a, st);
+    return launch_row_quant<256, 4, OP, FMT>(a, st);
+  }
+  switch ((vec + 511) / 512) {
+    case 3: return launch_row_quant<512, 3, OP, FMT>(a, st);
+    case 4: return launch_row_quant<512, 4, OP, FMT>(a, st);
+    case 5: return launch_row_quant<512, 5, OP, FMT>(a, st);
+    default: return launch_row_quant<512, 6, OP, FMT>(a, st);
+  }
+}
+
+template <int OP>
+sq_status row_quant(int fmt, const RowQuantArgs& a, cudaStream_t st) {
+  if (fmt == RQ_E4M3_GROUP) return row_quant<OP, RQ_E4M3_GROUP>(a, st);
+  if (fmt == RQ_I8_GROUP) return row_quant<OP, RQ_I8_GROUP>(a, st);
+  return row_quant<OP, RQ_I8_ROW>(a, st);
+}
+
+// Whether [p, p + n) and [q, q + m) share a byte.
+bool overlaps(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
+sq_status add_rmsnorm_quant(const void* h, const void* residual, const float* gamma, float eps,
+                            int fmt, void* residual_out, void* q, float* scales, float* inv_rms,
+                            int64_t M, int64_t K, void* stream) {
+  if (M < 0 || K <= 0 || K % 128 || K > kMaxStreamK) return SQ_ERR_SHAPE;
+  if (!(eps > 0.0f) || !(eps < 3.4e38f)) return SQ_ERR_SHAPE;
+  if (M > (1ll << 31) - 1) return SQ_ERR_SHAPE;
+  if (M == 0) return SQ_OK;
+  if (!h || !residual || !gamma || !residual_out || !q || !scales) return SQ_ERR_NULL;
+  if (!aligned16(h) || !aligned16(residual) || !aligned16(gamma) || !aligned16(residual_out) ||
+      !aligned16(q) || !aligned16(scales))
+    return SQ_ERR_ALIGN;
+  // in place means the same buffer: shifted, one row's sums would be read as another's inputs
+  const size_t bytes = static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
+  if ((residual_out != h && overlaps(residual_out, bytes, h, bytes)) ||
+      (residual_out != residual && overlaps(residual_out, bytes, residual, bytes)))
+    return SQ_ERR_SHAPE;
+  RowQuantArgs a{};
+  a.a = static_cast<const __nv_bfloat16*>(h);
+  a.b = static_cast<const __nv_bfloat16*>(residual);
+  a.b_out = static_cast<__nv_bfloat16*>(residual_out);
+  a.vec = gamma;
+  a.q = static_cast<uint8_t*>(q);
+  a.scales = scales;
+  a.r_out = inv_rms;
+  a.M = M;
+  a.K = static_cast<int>(K);
+  a.eps = eps;
+  return row_quant<RQ_ADD_NORM>(fmt, a, static_cast<cudaStream_t>(stream));
+}
+
+sq_status silu_mul_quant(const void* gate_up, const float* inv_smooth, int fmt, void* q,
+                         float* scales, int64_t M, int64_t K, void* stream) {
+  if (M < 0 || K <= 0 || K % 128 || K > kMaxStreamK) return SQ_ERR_SHAPE;
+  if (M > (1ll << 31) - 1) return SQ_ERR_SHAPE;
+  if (M == 0) return SQ_OK;
+  if (!gate_up || !q || !scales) return SQ_ERR_NULL;
+  if (!aligned16(gate_up) || !aligned16(q) || !aligned16(scales) ||
+      (inv_smooth && !aligned16(inv_smooth)))
+    return SQ_ERR_ALIGN;
+  RowQuantArgs a{};
+  a.a = static_cast<const __nv_bfloat16*>(gate_up);
+  a.vec = inv_smooth;
+  a.q = static_cast<uint8_t*>(q);
+  a.scales = scales;
+  a.M = M;
+  a.K = static_cast<int>(K);
+  return row_quant<RQ_SILU>(fmt, a, static_cast<cudaStream_t>(stream));
+}
+
+template <bool F8>
+sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows, const void* q_w,
+                         const float* s_w, const int32_t* offsets, void* y, int64_t T, int64_t M,
+                         int64_t E, int64_t N, int64_t K, cudaStream_t st) {
+  using Cfg = GroupedCfg<F8>;
+  const uint64_t k = static_cast<uint64_t>(K);
+  CUtensorMap tw, tx, tx64;
+  // one row per box for the gather; else 16- and 64-row boxes make up a tile's rows
+  if (!make_map(&tw, q_w, false, k, static_cast<uint64_t>(E * N), 128, 128) ||
+      !make_map(&tx, q_a, false, k, static_cast<uint64_t>(M), 128, rows ? 1 : 16) ||
+      !make_map(&tx64, q_a, false, k, static_cast<uint64_t>(M), 128, 64))
+    return SQ_ERR_CUDA;
+  static std::atomic<int> max_clusters[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SQ_ERR_CUDA;
+  const int smem = Cfg::smem_bytes();
+  int mc = max_clusters[dev].load(std::memory_order_acquire);
+  if (mc <= 0) {
+    if (cudaFuncSetAttribute(grouped_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+      return SQ_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(Cfg::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&mc, grouped_kernel<Cfg>, &cfg) != cudaSuccess || mc <= 0)
+      return SQ_ERR_CUDA;
+    max_clusters[dev].store(mc, std::memory_order_release);
+  }
+  GroupedArgs g{};
+  g.offsets = offsets;
+  g.rows = rows;
+  g.s_a = s_a;
+  g.s_w = s_w;
+  g.out = static_cast<__nv_bfloat16*>(y);
+  g.T = static_cast<int>(T);
+  g.M = static_cast<int>(M);
+  g.E = static_cast<int>(E);
+  g.N = static_cast<int>(N);
+  g.kb_total = static_cast<int>(K / 128);
+  g.tiles_n = static_cast<int>((N + 255) / 256);
+  // most tiles the offsets can give: each group of rows ends in at most one partial tile
+  const int64_t tiles = ((T < E ? T : E) + T / Cfg::BT) * g.tiles_n;
+  const int clusters = tiles < mc ? static_cast<int>(tiles) : mc;
+  return launch_dependent(grouped_kernel<Cfg>, static_cast<unsigned>(2 * clusters), Cfg::THREADS,
+                          smem, st, 2, tw, tx, tx64, g);
+}
+
+sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* rows,
+                     const void* q_w, const float* s_w, const int32_t* offsets, void* y, int64_t T,
+                     int64_t M, int64_t E, int64_t N, int64_t K, void* stream) {
+  const sq_status s = check_mnk(T, N, K);
+  if (s != SQ_OK) return s;
+  if (f8 && N % 128) return SQ_ERR_SHAPE;
+  if (E <= 0 || E > kMaxExperts) return SQ_ERR_SHAPE;
+  const int64_t most = (1ll << 31) - 1;
+  // coordinates and tile numbers are 32-bit
+  if (E * N + 256 > most || T + 256 > most) return SQ_ERR_SHAPE;
+  if ((E + T / 256 + 1) * ((N + 255) / 256) > most) return SQ_ERR_SHAPE;
+  if (M < 0 || M + 256 > most || (!rows && M != T)) return SQ_ERR_SHAPE;
+  if (T == 0) return SQ_OK;
+  if (M == 0) return SQ_ERR_SHAPE;
+  if (!q_a || !s_a || !q_w || !s_w || !offsets || !y) return SQ_ERR_NULL;
+  if (!aligned16(q_a) || !aligned16(s_a) || !aligned16(q_w) || !aligned16(s_w) ||
+      !aligned16(offsets) || !aligned16(y) || (rows && !aligned16(rows)))
+    return SQ_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return f8 ? launch_grouped<true>(q_a, s_a, rows, q_w, s_w, offsets, y, T, M, E, N, K, st)
+            : launch_grouped<false>(q_a, s_a, rows, q_w, s_w, offsets, y, T, M, E, N, K, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1011,6 +1222,52 @@ sq_status w8a16_group_mm(const void* x_bf16, const int8_t* q_w, const float* s_g
   // the reconstructed weights carry the scales: the epilogue stores the sums as they are
   return run_gemm(GK_BF16, x_bf16, wb, nullptr, nullptr, nullptr, y_bf16, M, N, K, workspace,
                   w_off, st);
+}
+
+// ---------------------------------------------------------------------------
+// Mixture-of-experts operators.
+
+sq_status sq_add_rmsnorm_quant(const void* h_bf16, const void* residual_bf16, const float* gamma,
+                               float eps, int64_t group, void* residual_out_bf16, int8_t* q_i8,
+                               float* scales, float* inv_rms, int64_t M, int64_t K, void* stream) {
+  if (group != 0 && group != K && group != 128) return SQ_ERR_SHAPE;
+  const int fmt = group == 128 && K != 128 ? RQ_I8_GROUP : RQ_I8_ROW;
+  return add_rmsnorm_quant(h_bf16, residual_bf16, gamma, eps, fmt, residual_out_bf16, q_i8, scales,
+                           inv_rms, M, K, stream);
+}
+
+sq_status sq_add_rmsnorm_quant_fp8(const void* h_bf16, const void* residual_bf16,
+                                   const float* gamma, float eps, void* residual_out_bf16,
+                                   uint8_t* q_e4m3, float* s_a, float* inv_rms, int64_t M,
+                                   int64_t K, void* stream) {
+  return add_rmsnorm_quant(h_bf16, residual_bf16, gamma, eps, RQ_E4M3_GROUP, residual_out_bf16,
+                           q_e4m3, s_a, inv_rms, M, K, stream);
+}
+
+sq_status sq_silu_mul_quant(const void* gate_up_bf16, const float* inv_smooth, int64_t group,
+                            int8_t* q_i8, float* scales, int64_t T, int64_t K, void* stream) {
+  if (group != 0 && group != K && group != 128) return SQ_ERR_SHAPE;
+  const int fmt = group == 128 && K != 128 ? RQ_I8_GROUP : RQ_I8_ROW;
+  return silu_mul_quant(gate_up_bf16, inv_smooth, fmt, q_i8, scales, T, K, stream);
+}
+
+sq_status sq_silu_mul_quant_fp8(const void* gate_up_bf16, const float* inv_smooth,
+                                uint8_t* q_e4m3, float* s_a, int64_t T, int64_t K, void* stream) {
+  return silu_mul_quant(gate_up_bf16, inv_smooth, RQ_E4M3_GROUP, q_e4m3, s_a, T, K, stream);
+}
+
+sq_status w8a8_grouped_mm(const int8_t* q_a, const float* s_tok, const int32_t* rows,
+                          const int8_t* q_w, const float* s_ch, const int32_t* offsets,
+                          void* y_bf16, int64_t T, int64_t M, int64_t E, int64_t N, int64_t K,
+                          void* stream) {
+  return grouped_mm(false, q_a, s_tok, rows, q_w, s_ch, offsets, y_bf16, T, M, E, N, K, stream);
+}
+
+sq_status fp8_block_grouped_mm(const uint8_t* q_a, const float* s_a, const int32_t* rows,
+                               const uint8_t* q_w, const float* s_w, const int32_t* offsets,
+                               void* y_bf16, int64_t T, int64_t M, int64_t E, int64_t N, int64_t K,
+                               void* stream) {
+  return grouped_mm(true, q_a, s_a, rows, q_w, s_w, offsets, y_bf16, T, M, E, N, K, stream);
 }
 
 sq_status sq_mma_peak(int kind, int iters, void* stream, double* ops_per_launch) {
