@@ -223,12 +223,17 @@ sq_status fp8_block_mm(const uint8_t* q_a, const float* s_a, const uint8_t* q_w,
 
 /* Residual addition + RMSNorm + SmoothQuant fold + dynamic INT8 quantisation.
  * Per row m: residual_out = bf16_rne(f32(h) + f32(residual)) (one fp32 rounding,
- * one to bf16), then sq_rmsnorm_quant's arithmetic on residual_out: scales per
- * row (group == 0 or K: fp32 [M]) or per 128 columns (group == 128: fp32
- * [M, K/128]).  h, residual, residual_out BF16 [M,K]; residual_out may be the
+ * one to bf16).  With x = residual_out: ss = sum_k f32(x)^2 accumulated in fp64
+ * and rounded once to fp32; r = 1 / sqrt(ss * f32(1/K) + eps) and v_k = (f32(x_k)
+ * * r) * gamma[k], each an IEEE fp32 operation; amax = max |v| over the row
+ * (group == 0 or K: scales fp32 [M]) or over each 128 columns (group == 128:
+ * scales fp32 [M, K/128]); scale = amax / 127, code = clamp(rint(v * f32(127 *
+ * f32(1 / amax))), -127, 127), round-half-even; amax == 0 gives scale 0 and zero
+ * codes.  (sq_rmsnorm_quant divides by K and by amax instead: a code next to a
+ * rounding border may differ by one from its answer.)  h, residual, residual_out BF16 [M,K]; residual_out may be the
  * residual or h itself (in place); one that overlaps them otherwise is refused
  * (SQ_ERR_SHAPE).  inv_rms (fp32 [M], may be NULL) receives r.  eps > 0; K <= 24576.
- * The factor 127 / amax is held at the largest finite fp32 (amax below about
+ * The factor of the codes is held at the largest finite fp32 (amax below about
  * 3.7e-37).  A row that holds inf or NaN has unspecified codes and scales; the
  * other rows are not affected.  The launch may overlap the tail of any
  * preceding kernel (it reads and writes nothing before that kernel's end). */
@@ -237,7 +242,7 @@ sq_status sq_add_rmsnorm_quant(const void* h_bf16, const void* residual_bf16, co
                                float* scales, float* inv_rms, int64_t M, int64_t K, void* stream);
 
 /* The same with OCP E4M3 codes and one scale per 128 columns (the arithmetic
- * of sq_quant_fp8_per_group on the normalised row): q_e4m3 [M,K] bit patterns,
+ * above with 448 for 127, code = e4m3_rne_satfinite): q_e4m3 [M,K] bit patterns,
  * s_a fp32 [M, K/128]. */
 sq_status sq_add_rmsnorm_quant_fp8(const void* h_bf16, const void* residual_bf16,
                                    const float* gamma, float eps, void* residual_out_bf16,
@@ -248,9 +253,9 @@ sq_status sq_add_rmsnorm_quant_fp8(const void* h_bf16, const void* residual_bf16
  * expert's (or an MLP's) two products.  gate_up BF16 [T, 2K]: columns 0..K-1 are
  * the gate g, K..2K-1 the other half u.  Per row: a = g / (1 + exp(-g)) * u in
  * fp32 (within 2^-20 of the exact value, or 2^-40 |u| absolutely), v =
- * a * inv_smooth[k] (inv_smooth fp32 [K], may be NULL: 1), then the codes and
- * scales of sq_quant_per_token (group == 0 or K) or of sq_quant_per_group
- * (group == 128) of v, with the factor 127 / amax held finite.  K % 128 == 0,
+ * a * inv_smooth[k] (inv_smooth fp32 [K], may be NULL: 1), then codes and scales
+ * of v as in sq_add_rmsnorm_quant, per row (group == 0 or K) or per 128 columns
+ * (group == 128).  K % 128 == 0,
  * K <= 24576.  Non-finite rows and the launch as for sq_add_rmsnorm_quant. */
 sq_status sq_silu_mul_quant(const void* gate_up_bf16, const float* inv_smooth, int64_t group,
                             int8_t* q_i8, float* scales, int64_t T, int64_t K, void* stream);

@@ -1,7 +1,8 @@
 // rowquant.cuh -- HBM-bound kernels that fuse a row operation with 8-bit
 // quantisation: residual addition + RMSNorm, and the gated activation
 // silu(gate) * up.  Codes are INT8 with one scale per row or per 128 columns, or
-// E4M3 with one scale per 128 columns (the arithmetic of quant.cuh).
+// E4M3 with one scale per 128 columns (as quant.cuh, with the
+// factors 127 / amax and 1 / K formed through one reciprocal).
 //
 // One pass over HBM: TPR threads own a row and hold it in registers (NV vectors
 // of 8 columns per thread) from the loads to the codes, so nothing is read
@@ -24,7 +25,7 @@ struct RowQuantArgs {
   float* r_out;             // 1/rms [M] or NULL
   int64_t M;
   int K;
-  float eps;
+  float eps, inv_k;         // inv_k = f32(1 / K)
 };
 
 // silu(g) * u = g / (1 + exp(-g)) * u.  The exponential and the quotient are the
@@ -33,6 +34,14 @@ struct RowQuantArgs {
 // the value is below 2^-40 |u|.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
+}
+
+// Values per code step: f32(QMAX * f32(1 / amax)), held finite (a largest
+// magnitude below 2^-119 would make it infinite, and zeros NaN).  With |v| <=
+// amax the product stays below QMAX (1 + 2^-24)^4: INT8 rounds it to at most 127,
+// E4M3 saturates at 448.
+__device__ __forceinline__ float code_factor(float amax, float qmax) {
+  return fminf(__fmul_rn(qmax, __frcp_rn(amax)), 3.402823466e38f);
 }
 
 template <int TPR, int NV, int OP, int FMT>
@@ -102,7 +111,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 #pragma unroll
         for (int w = 0; w < NW; ++w) ss += red_d[slot][rib][w];
       }
-      const float ms = __fdiv_rn(__double2float_rn(ss), static_cast<float>(K));
+      const float ms = __fmul_rn(__double2float_rn(ss), p.inv_k);
       const float rn = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
       if (active && p.r_out && t == 0) p.r_out[row] = rn;
 #pragma unroll
@@ -174,8 +183,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + t) * 8;
       const float am = GROUP ? gmax[j] : amax;
-      // held finite: a largest magnitude below 2^-119 would make it infinite, and zeros NaN
-      const float mult = am > 0.0f ? fminf(__fdiv_rn(QMAX, am), 3.402823466e38f) : 0.0f;
+      const float mult = am > 0.0f ? code_factor(am, QMAX) : 0.0f;
       if (!active || c >= K) continue;
       if (GROUP && (t & 15) == 0) p.scales[row * (K >> 7) + (c >> 7)] = __fdiv_rn(am, QMAX);
       uint32_t pk[2];

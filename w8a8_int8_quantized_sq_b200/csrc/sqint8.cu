@@ -759,6 +759,7 @@ sq_status add_rmsnorm_quant(const void* h, const void* residual, const float* ga
   a.M = M;
   a.K = static_cast<int>(K);
   a.eps = eps;
+  a.inv_k = 1.0f / static_cast<float>(K);
   return row_quant<RQ_ADD_NORM>(fmt, a, static_cast<cudaStream_t>(stream));
 }
 
