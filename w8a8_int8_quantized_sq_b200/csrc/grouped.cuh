@@ -47,29 +47,96 @@ struct GroupedArgs {
   int tiles_n;             // ceil(N / 256)
 };
 
+// Tensor maps of the token rows: boxes of 16, 32, 64 and 128 rows, of which a tile
+// takes the smallest that holds its half (one load per stage and CTA: a load's cost
+// is mostly its own, a 96-row half fetched as 64 + 16 + 16 rows made the prefill of
+// 32768 rows over 64 experts, K = N = 2048, take 167 us); [0] has one-row
+// boxes when the tokens are gathered.
+struct GroupedMaps {
+  CUtensorMap m[4];
+};
+
 template <bool F8_>
 struct GroupedCfg {
   static constexpr bool F8 = F8_;
-  static constexpr int BT = 256;                 // most tokens per tile
-  static constexpr int STAGES = F8 ? 5 : 6;
+  static constexpr int BT = F8 ? 128 : 256;      // most tokens per tile
+  static constexpr int NACC = 512 / BT;          // accumulators (BT tensor-memory columns each)
+  static constexpr int STAGES = 6;
   static constexpr int A_BYTES = 128 * 128;      // weights staged by each CTA per K block
-  static constexpr int B_BYTES = BT / 2 * 128;   // tokens staged by each CTA per K block
-  static constexpr int NACC = 2;
+  static constexpr int B_BYTES = BT / 2 * 128;   // tokens staged by each CTA per K block, at most
   static constexpr int TMEM_COLS = 512;
+  static constexpr int NG = F8 ? 5 : 8;          // warps that issue gather loads
   static constexpr int NE = F8 ? 16 : 8;         // epilogue warps
-  static constexpr int EPI0 = F8 ? 3 : 2;        // first epilogue warp
+  static constexpr int CPT = F8 ? BT / (NE / 4) : 32;  // accumulator columns per warp and pass
+  static constexpr int EPI0 = 3 + NG;            // first epilogue warp
   static constexpr int THREADS = (EPI0 + NE) * 32;
-  static constexpr int SRING = 8;                // FP8: scale vectors in the ring
+  static constexpr int SRING = F8 ? 16 : 8;      // scale vectors in the ring
+  static constexpr int PITCH = 80;               // bytes per token in a warp's store staging
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SC = OFF_B + STAGES * B_BYTES;
-  static constexpr int OFF_LO = OFF_SC + (F8 ? SRING * BT * 4 : 0);
+  static constexpr int OFF_ST = OFF_SC + SRING * BT * 4;
+  static constexpr int OFF_LO = OFF_ST + NE * 16 * PITCH;
   static constexpr int OFF_CUM = OFF_LO + (kMaxExperts + 1) * 4;
   static constexpr int OFF_BAR = (OFF_CUM + (kMaxExperts + 1) * 4 + 7) & ~7;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * NACC + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int smem_bytes() { return 1024 + OFF_MISC + 16; }
   static_assert(1024 + OFF_MISC + 16 <= 232448, "shared memory");
+  static_assert(SRING >= 2 * NACC + 4, "scale ring, see the scale warp");
 };
+
+// mbarrier wait without a suspend-time hint, bounded like wait_bounded, the same
+// answer in every lane.  The accumulators' round trip (MMA, commit, epilogue,
+// release, MMA) is made of such waits: with the 20 us hint of the other kernels
+// it took 8 % longer.
+__device__ __forceinline__ bool grouped_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool grouped_wait_lane(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const uint32_t a = smem_u32(bar);
+  if (grouped_try_wait(a, parity)) return true;
+  const long long t0 = sm_cycles();
+  for (;;) {
+    if (grouped_try_wait(a, parity)) return true;
+    if (*abort_flag) return false;
+    if (sm_cycles() - t0 > kWaitLimitCycles) {
+      *abort_flag = 1;
+      atomicOr(&g_error_word, kErrTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool grouped_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, grouped_wait_lane(bar, parity, abort_flag));
+}
+
+// Asynchronous load of 16 columns of 16 tensor-memory lanes (taddr: lane 0 or 16 of
+// the warp's quadrant) as matrix fragments: lane l gets, for columns 8 i + 2 (l % 4)
+// and the next, rows l / 4 (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]).
+// A lane sees a quarter of the columns, so the per-token scales are four times fewer
+// reads than with one lane per channel.
+__device__ __forceinline__ void tmem_frag16_async(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+// Completes this thread's tensor-memory loads; r's values may be used after it.
+__device__ __forceinline__ void tmem_frag_wait(uint32_t (&r)[8], uint32_t (&s)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(s[0]), "+r"(s[1]), "+r"(s[2]), "+r"(s[3]), "+r"(s[4]), "+r"(s[5]),
+                 "+r"(s[6]), "+r"(s[7])::"memory");
+}
 
 // 2-D four-row gather load (rows r.x .. r.w of the tensor, 128 bytes each at
 // innermost coordinate x) into this CTA's shared memory; bytes counted on the
@@ -89,20 +156,23 @@ struct GroupedTile {
   int e, ct, row0, nrows;
 };
 
-// Walks this cluster's tiles in order; cum[e] counts the token tiles of the
-// experts before e.
+// The tile list: expert by expert, channel tile by channel tile, the token tiles of a
+// weight tile next to each other.  cum[e] counts the token tiles of the experts before e.
 struct GroupedWalk {
   const int* lo;
   const int* cum;
   int tiles_n, e;
   __device__ __forceinline__ GroupedWalk(const int* lo_, const int* cum_, int tiles_n_)
       : lo(lo_), cum(cum_), tiles_n(tiles_n_), e(0) {}
+  // rows per token tile of an expert with r rows in nt tiles (at most BT)
+  static __device__ __forceinline__ int width(int r, int nt) { return ((r + nt - 1) / nt + 31) & ~31; }
+  // tile t; t must not decrease from call to call
   __device__ __forceinline__ GroupedTile at(int t) {
     while (t >= cum[e + 1] * tiles_n) ++e;
     const int nt = cum[e + 1] - cum[e];
     const int i = t - cum[e] * tiles_n;
     const int r = lo[e + 1] - lo[e];
-    const int w = ((r + nt - 1) / nt + 31) & ~31;  // rows per token tile, at most BT
+    const int w = width(r, nt);
     GroupedTile g;
     g.e = e;
     g.ct = i / nt;
@@ -113,22 +183,40 @@ struct GroupedWalk {
   }
 };
 
-// Two tokens' values of this lane's channel -> 32-bit stores of two channels:
-// even lanes store token a (channels l, l + 1), odd lanes token b (l - 1, l).
-__device__ __forceinline__ void grouped_store2(__nv_bfloat16* oa, __nv_bfloat16* ob, float a,
-                                               float b, int lane, bool ok_a, bool ok_b) {
-  const bool odd = lane & 1;
-  const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-  const uint32_t v = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-  if (odd ? ok_b : ok_a) *reinterpret_cast<uint32_t*>(odd ? ob - 1 : oa) = v;
+// Stores 16 tokens x 32 channels of one warp as bf16.  p[b][k]: this lane's fragment
+// of tokens 8 b .. 8 b + 7 and channels 8 k .. 8 k + 7 (its row is the channel, its two
+// values two tokens).  A transposing matrix store puts every token's 32 channels
+// side by side in the warp's staging rows, which leave in 16-byte pieces.
+// out: token 0, channel 0 of the block; the first ntok tokens are stored; ch_ok:
+// channels 8 (lane % 4) .. + 7 exist.
+template <int PITCH>
+__device__ __forceinline__ void grouped_store(uint32_t st, __nv_bfloat16* out, size_t N, int lane,
+                                              const uint32_t (&p)[2][4], int ntok, bool ch_ok) {
+  const uint32_t to = st + (lane & 7) * PITCH + (lane >> 3) * 16;
+  __syncwarp();  // the previous block has been read
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     to + b * 8 * PITCH),
+                 "r"(p[b][0]), "r"(p[b][1]), "r"(p[b][2]), "r"(p[b][3])
+                 : "memory");
+  __syncwarp();
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int t = b * 8 + (lane >> 2);
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(st + t * PITCH + (lane & 3) * 16)
+                 : "memory");
+    if (t < ntok && ch_ok) *reinterpret_cast<uint4*>(out + t * N + (lane & 3) * 8) = v;
+  }
 }
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmW,    // weights [E N, K], 128-row boxes
-                   const __grid_constant__ CUtensorMap tmX,    // tokens [M, K]: 16-row boxes, or
-                                                               // one-row boxes for the gather
-                   const __grid_constant__ CUtensorMap tmX64,  // tokens, 64-row boxes
+    grouped_kernel(const __grid_constant__ CUtensorMap tmW,   // weights [E N, K], 128-row boxes
+                   const __grid_constant__ GroupedMaps tmX,   // tokens
                    const GroupedArgs g) {
   constexpr int STAGES = Cfg::STAGES, NACC = Cfg::NACC, NE = Cfg::NE, BT = Cfg::BT;
   extern __shared__ uint8_t smem_raw[];
@@ -161,7 +249,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       mbar_init(empty + s, 1);
     }
     for (int a = 0; a < NACC; ++a) {
-      mbar_init(tfull + a, Cfg::F8 ? 2 : 1);
+      mbar_init(tfull + a, 2);
       mbar_init(tempty + a, 2 * NE);
     }
     mbar_init(drain, 1);
@@ -172,10 +260,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tmem_alloc_pair(tmem_holder, Cfg::TMEM_COLS);
     tmem_relinquish_pair();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
-  }
+  if (warp == 0 && lane == 0) tma_prefetch_desc(&tmW);
   griddep_wait();  // nothing above touches global memory: the launch may overlap any kernel
   // offsets, held inside [0, T] and non-decreasing whatever the caller wrote
   for (int e = threadIdx.x; e <= g.E; e += Cfg::THREADS) lo[e] = min(max(__ldg(g.offsets + e), 0), g.T);
@@ -219,63 +304,46 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   griddep_launch_dependents();
 
   if (warp == 0) {
-    // ------------------------------------------------------ TMA producer
-    const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
-    const uint64_t pol = policy_evict_normal();
-    GroupedWalk walk(lo, cum, g.tiles_n);
-    uint32_t stage = 0, phase = 0;
-    long long fills = 0;
-    bool ok = true;
-    for (int t = cluster; ok && t < num_tiles; t += nclusters) {
-      const GroupedTile tile = walk.at(t);
-      const int half = ((tile.nrows + 31) & ~31) >> 1;  // token rows staged by this CTA
-      const int w_row = tile.e * g.N + tile.ct * 256 + static_cast<int>(rank) * 128;
-      const int first = static_cast<int>(rank) * half;
-      int4 r4 = make_int4(g.M, g.M, g.M, g.M);
-      if (g.rows && lane * 4 < half) {
-        // rows past the tile or outside the tokens are fetched as zeros
-        auto token = [&](int i) {
-          if (first + i >= tile.nrows) return g.M;
-          const int r = __ldg(g.rows + tile.row0 + first + i);
-          return static_cast<unsigned>(r) < static_cast<unsigned>(g.M) ? r : g.M;
-        };
-        r4 = make_int4(token(lane * 4), token(lane * 4 + 1), token(lane * 4 + 2), token(lane * 4 + 3));
-      }
-      for (int kb = 0; kb < kbt; ++kb) {
-        if (!warp_wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        uint8_t* dst = smB + stage * Cfg::B_BYTES;
-        if (lane == 0) {
-          if (leader) mbar_arrive_expect_tx(full + stage, 2 * (Cfg::A_BYTES + half * 128));
+    // ------------------------------- weights, and tokens in row order (TMA)
+    if (lane == 0) {
+      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+      const uint64_t pol = policy_evict_normal();
+      GroupedWalk walk(lo, cum, g.tiles_n);
+      uint32_t stage = 0, phase = 0;
+      long long fills = 0;
+      bool ok = true;
+      for (int t = cluster; ok && t < num_tiles; t += nclusters) {
+        const GroupedTile tile = walk.at(t);
+        const int half = ((tile.nrows + 31) & ~31) >> 1;  // token rows staged by this CTA
+        const int w_row = tile.e * g.N + tile.ct * 256 + static_cast<int>(rank) * 128;
+        const int x_row = tile.row0 + static_cast<int>(rank) * half;
+        // the smallest box of 16 << box rows that holds the half
+        const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        const uint32_t bytes = 2 * (Cfg::A_BYTES + (g.rows ? half : 16 << box) * 128);
+        for (int kb = 0; kb < kbt; ++kb) {
+          if (!grouped_wait_lane(empty + stage, phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(full + stage, bytes);
           tma_load_2d_pair(smA + stage * Cfg::A_BYTES, &tmW, kb * 128, w_row,
                            full_leader + stage * 8, pol);
-          if (!g.rows) {
-            int i = 0;
-            for (; i + 64 <= half; i += 64)
-              tma_load_2d_pair(dst + i * 128, &tmX64, kb * 128, tile.row0 + first + i,
-                               full_leader + stage * 8, pol);
-            for (; i < half; i += 16)
-              tma_load_2d_pair(dst + i * 128, &tmX, kb * 128, tile.row0 + first + i,
-                               full_leader + stage * 8, pol);
+          if (!g.rows)
+            tma_load_2d_pair(smB + stage * Cfg::B_BYTES, &tmX.m[box], kb * 128, x_row,
+                             full_leader + stage * 8, pol);
+          ++fills;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-        if (g.rows && lane * 4 < half)
-          tma_gather4_pair(dst + lane * 512, &tmX, kb * 128, r4, full_leader + stage * 8);
-        __syncwarp();
-        ++fills;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-    }
-    if (leader && lane == 0) {
-      // the pair's copies (both CTAs' bytes count here) have all landed
-      for (int st = 0; st < STAGES; ++st) {
-        const long long n = fills / STAGES + (st < fills % STAGES ? 1 : 0);
-        if (n > 0) wait_drain(full + st, static_cast<uint32_t>((n - 1) & 1));
+      if (leader) {
+        // the pair's copies (both CTAs' bytes count here) have all landed
+        for (int st = 0; st < STAGES; ++st) {
+          const long long n = fills / STAGES + (st < fills % STAGES ? 1 : 0);
+          if (n > 0) wait_drain(full + st, static_cast<uint32_t>((n - 1) & 1));
+        }
       }
     }
     __syncwarp();
@@ -294,10 +362,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (Cfg::F8 || kb == 0) {  // a free accumulator: per K block (FP8) or per tile
             const uint32_t a = local % NACC, u = local / NACC;
             ++local;
-            if (!warp_wait_bounded(tempty + a, (u & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+            if (!grouped_wait(tempty + a, (u & 1u) ^ 1u, abort_flag)) { ok = false; break; }
             d = tmem + a * BT;
           }
-          if (!warp_wait_bounded(full + stage, phase, abort_flag)) { ok = false; break; }
+          if (!grouped_wait(full + stage, phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = smem_u32(smA + stage * Cfg::A_BYTES);
           const uint32_t sb = smem_u32(smB + stage * Cfg::B_BYTES);
@@ -323,61 +391,144 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (Cfg::F8 && warp == 2) {
+  } else if (warp >= 3 && warp < Cfg::EPI0) {
+    // ---------------------------------------------------- gathered tokens
+    // Each lane fetches four rows of a stage; lane l of warp w takes rows 4 (NG l +
+    // w) and up, so that the warps share the loads evenly.  A load takes its warp
+    // about 80 cycles to issue: from one warp alone they made the prefill of
+    // 32768 rows over 64 experts, K = N = 2048, take 346 us, from four 152 us,
+    // from eight 140 us.
+    if (g.rows) {
+      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+      const int j = (lane * Cfg::NG + warp - 3) * 4;
+      GroupedWalk walk(lo, cum, g.tiles_n);
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int t = cluster; ok && t < num_tiles; t += nclusters) {
+        const GroupedTile tile = walk.at(t);
+        const int half = ((tile.nrows + 31) & ~31) >> 1;
+        const int first = static_cast<int>(rank) * half + j;
+        // rows past the tile or outside the tokens are fetched as zeros
+        auto token = [&](int i) {
+          if (first + i >= tile.nrows) return g.M;
+          const int r = __ldg(g.rows + tile.row0 + first + i);
+          return static_cast<unsigned>(r) < static_cast<unsigned>(g.M) ? r : g.M;
+        };
+        const bool mine = j < half;
+        int4 r4 = make_int4(g.M, g.M, g.M, g.M);
+        if (mine) r4 = make_int4(token(0), token(1), token(2), token(3));
+        for (int kb = 0; kb < kbt; ++kb) {
+          if (!grouped_wait(empty + stage, phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (mine)
+            tma_gather4_pair(smB + stage * Cfg::B_BYTES + j * 128, &tmX.m[0], kb * 128, r4,
+                             full_leader + stage * 8);
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 2) {
     // ------------------------------------------------------------- scales
-    // Vector kb of the ring slot kb % SRING: s_a[token, kb] * s_w[block, kb] for the
-    // tile's tokens (0 for rows outside).  A slot is rewritten SRING K blocks
-    // later; by then this warp has seen the accumulator of K block kb - 3
-    // complete, whose buffer the epilogue released (after using its scales) for
-    // K block kb - 5, so slots up to kb - 6 are free.
+    // One vector per accumulator, in ring slot (its number) % SRING: INT8 s_tok of
+    // the tile's tokens, FP8 s_a[token, kb] * s_w[block, kb] (0 for rows outside).
+    // When accumulator n is published, n - NACC is known to be complete; its buffer
+    // had been released for it by an epilogue that was done with n - 2 NACC - 1.  So
+    // the slots still in use are those of n - 2 NACC .. n, and with SRING >= 2 NACC +
+    // 4 the four vectors before the next one to be published may be written.
+    constexpr int NV = BT / 32;  // 32-token vectors of a tile
     GroupedWalk walk(lo, cum, g.tiles_n);
     uint32_t local = 0;
     bool ok = true;
+    // the accumulator's scales are in the ring; its barrier's previous use must be over
+    auto publish = [&]() {
+      const uint32_t a = local % NACC, u = local / NACC;
+      if (u > 0 && !grouped_wait(tfull + a, (u - 1u) & 1u, abort_flag)) return false;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tfull + a);
+      ++local;
+      return true;
+    };
     for (int t = cluster; ok && t < num_tiles; t += nclusters) {
       const GroupedTile tile = walk.at(t);
-      const int nch = (tile.nrows + 31) >> 5;  // 32-token chunks
-      const int ch0 = tile.ct * 256 + static_cast<int>(rank) * 128;
-      const bool ch_ok = ch0 < g.N;
-      const float* sw = g.s_w + (static_cast<size_t>(tile.e) * (g.N >> 7) + (ch_ok ? ch0 >> 7 : 0)) * kbt;
-      const float* sa[BT / 32];
+      int tok[NV];  // token of column 32 i + lane, -1: none
 #pragma unroll
-      for (int i = 0; i < BT / 32; ++i) {
-        sa[i] = nullptr;
+      for (int i = 0; i < NV; ++i) {
         const int c = i * 32 + lane;
+        tok[i] = -1;
         if (c < tile.nrows) {
           const int r = g.rows ? __ldg(g.rows + tile.row0 + c) : tile.row0 + c;
-          if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M))
-            sa[i] = g.s_a + static_cast<size_t>(r) * kbt;
+          if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M)) tok[i] = r;
         }
       }
-      float v[BT / 32], w = __ldg(sw);
-#pragma unroll
-      for (int i = 0; i < BT / 32; ++i) v[i] = i < nch && sa[i] ? __ldg(sa[i]) : 0.0f;
-      for (int kb = 0; kb < kbt; ++kb, ++local) {
+      if constexpr (!Cfg::F8) {
         float* slot = ring + (local % Cfg::SRING) * BT;
 #pragma unroll
-        for (int i = 0; i < BT / 32; ++i)
-          if (i < nch) slot[i * 32 + lane] = __fmul_rn(v[i], w);
-        if (kb + 1 < kbt) {
-          w = __ldg(sw + kb + 1);
+        for (int i = 0; i < NV; ++i) slot[i * 32 + lane] = tok[i] >= 0 ? __ldg(g.s_a + tok[i]) : 0.0f;
+        ok = publish();
+      } else {
+        const int ch0 = tile.ct * 256 + static_cast<int>(rank) * 128;
+        const float* sw = g.s_w + (static_cast<size_t>(tile.e) * (g.N >> 7) + (ch0 < g.N ? ch0 >> 7 : 0)) * kbt;
+        const bool wide = (kbt & 3) == 0;  // a token's scales can be loaded four K blocks at a time
+        float4 v[NV], w;
+        // scales of K blocks kb .. kb + 3 (0 past the last)
+        auto load4 = [&](const float* p, int kb) {
+          if (wide) return __ldg(reinterpret_cast<const float4*>(p + kb));
+          return make_float4(__ldg(p + kb), kb + 1 < kbt ? __ldg(p + kb + 1) : 0.0f,
+                             kb + 2 < kbt ? __ldg(p + kb + 2) : 0.0f,
+                             kb + 3 < kbt ? __ldg(p + kb + 3) : 0.0f);
+        };
+        auto fetch = [&](int kb) {
+          w = load4(sw, kb);
 #pragma unroll
-          for (int i = 0; i < BT / 32; ++i)
-            if (i < nch) v[i] = sa[i] ? __ldg(sa[i] + kb + 1) : 0.0f;
+          for (int i = 0; i < NV; ++i)
+            v[i] = tok[i] >= 0 ? load4(g.s_a + static_cast<size_t>(tok[i]) * kbt, kb)
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        };
+        uint32_t next = local;  // accumulator of the next vector to write
+        auto put = [&](float w_j, auto part) {
+          float* slot = ring + (next++ % Cfg::SRING) * BT;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) slot[i * 32 + lane] = __fmul_rn(part(v[i]), w_j);
+        };
+        auto put_j = [&](int j) {
+          if (j == 0) put(w.x, [](const float4& f) { return f.x; });
+          else if (j == 1) put(w.y, [](const float4& f) { return f.y; });
+          else if (j == 2) put(w.z, [](const float4& f) { return f.z; });
+          else put(w.w, [](const float4& f) { return f.w; });
+        };
+        // four vectors ahead of the published ones, the loads of four more in flight
+        fetch(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < kbt) put_j(j);
+        if (4 < kbt) fetch(4);
+        for (int kb = 0; ok && kb < kbt; kb += 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (ok && kb + j < kbt) {
+              ok = publish();
+              if (kb + 4 + j < kbt) put_j(j);
+            }
+          }
+          if (kb + 8 < kbt) fetch(kb + 8);
         }
-        const uint32_t a = local % NACC, u = local / NACC;
-        // the previous use of this barrier must be over before its next arrival
-        if (u > 0 && !warp_wait_bounded(tfull + a, (u - 1u) & 1u, abort_flag)) { ok = false; break; }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tfull + a);
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int ew = warp - Cfg::EPI0;
-    const int q = warp & 3;                 // tensor-memory lane quadrant
+    const int q = warp & 3;                 // tensor-memory lane quadrant: 32 channels
     const int grp = ew >> 2;                // which columns of the tile
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t st = smem_u32(smem + Cfg::OFF_ST + ew * 16 * Cfg::PITCH);
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
+    const size_t N = static_cast<size_t>(g.N);
     auto release = [&](uint32_t a) {
       tc_fence_before();
       __syncwarp();
@@ -391,35 +542,49 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     bool ok = true;
     for (int t = cluster; ok && t < num_tiles; t += nclusters) {
       const GroupedTile tile = walk.at(t);
-      const int ch = tile.ct * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const bool ch_ok = ch < g.N;
+      const int ch = tile.ct * 256 + static_cast<int>(rank) * 128 + q * 32;  // this warp's channels
+      const bool ch_ok = ch + (lane & 3) * 8 < g.N;
       const int n = (tile.nrows + 31) & ~31;
-      __nv_bfloat16* out = g.out + static_cast<size_t>(tile.row0) * g.N + ch;
+      __nv_bfloat16* out = g.out + static_cast<size_t>(tile.row0) * N + ch;
       if constexpr (!Cfg::F8) {
-        const float s_ch = ch_ok ? __ldg(g.s_w + static_cast<size_t>(tile.e) * g.N + ch) : 0.0f;
+        float s_ch[4];  // of channels 8 k + lane / 4
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = ch + 8 * k + (lane >> 2);
+          s_ch[k] = c < g.N ? __ldg(g.s_w + static_cast<size_t>(tile.e) * N + c) : 0.0f;
+        }
         const uint32_t a = local % NACC, u = local / NACC;
+        const float* slot = ring + (local % Cfg::SRING) * BT;
         ++local;
-        if (!warp_wait_bounded(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
+        if (!grouped_wait(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
+        const uint32_t src = lanes + a * BT;
 #pragma unroll 1
         for (int c = grp * 32; c < n; c += (NE / 4) * 32) {
-          // lane j holds the scale of column c + j (0: no such token)
-          float st = 0.0f;
-          if (c + lane < tile.nrows) {
-            const int r = g.rows ? __ldg(g.rows + tile.row0 + c + lane) : tile.row0 + c + lane;
-            if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M)) st = __ldg(g.s_a + r);
-          }
-          uint32_t v[32];
-          tmem_ld32(lane_base + a * BT + c, v);
-          __nv_bfloat16* o = out + static_cast<size_t>(c) * g.N;
+          uint32_t v[2][2][8];  // [16 columns][16 channels]
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float s0 = __shfl_sync(0xffffffffu, st, j), s1 = __shfl_sync(0xffffffffu, st, j + 1);
-            const float y0 = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(v[j])), s0), s_ch);
-            const float y1 = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(v[j + 1])), s1), s_ch);
-            grouped_store2(o, o + g.N, y0, y1, lane, ch_ok && c + j < tile.nrows,
-                           ch_ok && c + j + 1 < tile.nrows);
-            o += 2 * static_cast<size_t>(g.N);
+          for (int i = 0; i < 2; ++i) {
+            tmem_frag16_async(src + c + i * 16, v[i][0]);
+            tmem_frag16_async(src + c + i * 16 + (16u << 16), v[i][1]);
+          }
+          tmem_frag_wait(v[0][0], v[0][1]);
+          tmem_frag_wait(v[1][0], v[1][1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t pk[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float2 s = *reinterpret_cast<const float2*>(slot + c + i * 16 + b * 8 + (lane & 3) * 2);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t* x = &v[i][k >> 1][4 * b + 2 * (k & 1)];
+                pk[b][k] = pack_bf16x2(
+                    __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(x[0])), s.x), s_ch[k]),
+                    __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(x[1])), s.y), s_ch[k]));
+              }
+            }
+            grouped_store<Cfg::PITCH>(st, out + (c + i * 16) * N, N, lane, pk,
+                                      tile.nrows - c - i * 16, ch_ok);
           }
         }
         release(a);
@@ -428,41 +593,58 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int wcol = ((n >> 2) + 15) & ~15;
         const int col0 = grp * wcol;
         const int ncol = max(0, min(wcol, n - col0));
-        float acc[64];
+        constexpr int NC = Cfg::CPT / 16;
+        float acc[NC][2][8];
 #pragma unroll
-        for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+        for (int j = 0; j < NC * 16; ++j) (&acc[0][0][0])[j] = 0.0f;
         for (int kb = 0; kb < kbt; ++kb, ++local) {
           const uint32_t a = local % NACC, u = local / NACC;
-          if (!warp_wait_bounded(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
+          if (!grouped_wait(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const float4* sc = reinterpret_cast<const float4*>(ring + (local % Cfg::SRING) * BT + col0);
+          const float* slot = ring + (local % Cfg::SRING) * BT + col0 + (lane & 3) * 2;
+          const uint32_t src = lanes + a * BT + col0;
+          uint32_t v[NC][2][8];
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            if (c < ncol) {
-              uint32_t v[16];
-              tmem_ld16(lane_base + a * BT + col0 + c, v);
-              if (c + 16 >= ncol) release(a);
+          for (int i = 0; i < NC; ++i)
+            if (i * 16 < ncol) {
+              tmem_frag16_async(src + i * 16, v[i][0]);
+              tmem_frag16_async(src + i * 16 + (16u << 16), v[i][1]);
+            }
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 s = sc[(c + j) >> 2];
-                acc[c + j] = __fmaf_rn(__uint_as_float(v[j]), s.x, acc[c + j]);
-                acc[c + j + 1] = __fmaf_rn(__uint_as_float(v[j + 1]), s.y, acc[c + j + 1]);
-                acc[c + j + 2] = __fmaf_rn(__uint_as_float(v[j + 2]), s.z, acc[c + j + 2]);
-                acc[c + j + 3] = __fmaf_rn(__uint_as_float(v[j + 3]), s.w, acc[c + j + 3]);
+          for (int i = 0; i < NC; ++i) tmem_frag_wait(v[i][0], v[i][1]);
+          release(a);  // the K block is in registers
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            if (i * 16 < ncol) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const float2 s = *reinterpret_cast<const float2*>(slot + i * 16 + b * 8);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) {
+                    float* x = &acc[i][h][4 * b + 2 * r];
+                    x[0] = __fmaf_rn(__uint_as_float(v[i][h][4 * b + 2 * r]), s.x, x[0]);
+                    x[1] = __fmaf_rn(__uint_as_float(v[i][h][4 * b + 2 * r + 1]), s.y, x[1]);
+                  }
               }
             }
-          }
-          if (ncol == 0) release(a);
         }
         if (!ok) break;
-        __nv_bfloat16* o = out + static_cast<size_t>(col0) * g.N;
 #pragma unroll
-        for (int j = 0; j < 64; j += 2) {
-          if (j < ncol)
-            grouped_store2(o, o + g.N, acc[j], acc[j + 1], lane, ch_ok && col0 + j < tile.nrows,
-                           ch_ok && col0 + j + 1 < tile.nrows);
-          o += 2 * static_cast<size_t>(g.N);
-        }
+        for (int i = 0; i < NC; ++i)
+          if (i * 16 < ncol) {
+            uint32_t pk[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float* x = &acc[i][k >> 1][4 * b + 2 * (k & 1)];
+                pk[b][k] = pack_bf16x2(x[0], x[1]);
+              }
+            grouped_store<Cfg::PITCH>(st, out + (col0 + i * 16) * N, N, lane, pk,
+                                      tile.nrows - col0 - i * 16, ch_ok);
+          }
       }
     }
   }

@@ -788,12 +788,18 @@ sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows,
                          int64_t E, int64_t N, int64_t K, cudaStream_t st) {
   using Cfg = GroupedCfg<F8>;
   const uint64_t k = static_cast<uint64_t>(K);
-  CUtensorMap tw, tx, tx64;
-  // one row per box for the gather; else 16- and 64-row boxes make up a tile's rows
-  if (!make_map(&tw, q_w, false, k, static_cast<uint64_t>(E * N), 128, 128) ||
-      !make_map(&tx, q_a, false, k, static_cast<uint64_t>(M), 128, rows ? 1 : 16) ||
-      !make_map(&tx64, q_a, false, k, static_cast<uint64_t>(M), 128, 64))
-    return SQ_ERR_CUDA;
+  CUtensorMap tw;
+  GroupedMaps tx{};
+  if (!make_map(&tw, q_w, false, k, static_cast<uint64_t>(E * N), 128, 128)) return SQ_ERR_CUDA;
+  if (rows) {
+    if (!make_map(&tx.m[0], q_a, false, k, static_cast<uint64_t>(M), 128, 1)) return SQ_ERR_CUDA;
+  } else {
+    // boxes up to the half of the largest tile that T rows can make
+    const int64_t most = T < Cfg::BT ? T : Cfg::BT;
+    for (int i = 0; i < 4 && (i == 0 || (16 << (i - 1)) < (most + 31) / 32 * 16); ++i)
+      if (!make_map(&tx.m[i], q_a, false, k, static_cast<uint64_t>(M), 128, 16u << i))
+        return SQ_ERR_CUDA;
+  }
   static std::atomic<int> max_clusters[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SQ_ERR_CUDA;
@@ -834,7 +840,7 @@ sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows,
   const int64_t tiles = ((T < E ? T : E) + T / Cfg::BT) * g.tiles_n;
   const int clusters = tiles < mc ? static_cast<int>(tiles) : mc;
   return launch_dependent(grouped_kernel<Cfg>, static_cast<unsigned>(2 * clusters), Cfg::THREADS,
-                          smem, st, 2, tw, tx, tx64, g);
+                          smem, st, 2, tw, tx, g);
 }
 
 sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* rows,
