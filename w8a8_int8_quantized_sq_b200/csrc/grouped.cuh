@@ -65,31 +65,38 @@ struct GroupedCfg {
   static constexpr int A_BYTES = 128 * 128;      // weights staged by each CTA per K block
   static constexpr int B_BYTES = BT / 2 * 128;   // tokens staged by each CTA per K block, at most
   static constexpr int TMEM_COLS = 512;
-  static constexpr int NG = F8 ? 5 : 8;          // warps that issue gather loads
-  static constexpr int NE = F8 ? 16 : 8;         // epilogue warps
-  static constexpr int CPT = F8 ? BT / (NE / 4) : 32;  // accumulator columns per warp and pass
-  static constexpr int EPI0 = 3 + NG;            // first epilogue warp
+  static constexpr int NS = F8 ? 2 : 1;          // scale warps
+  static constexpr int NG = F8 ? 4 : 8;          // warps that issue gather loads
+  static constexpr int NE = 8;                   // epilogue warps
+  static constexpr int EPI0 = 2 + NS + NG;       // first epilogue warp
   static constexpr int THREADS = (EPI0 + NE) * 32;
-  static constexpr int SRING = F8 ? 16 : 8;      // scale vectors in the ring
+  static constexpr int SV = F8 ? 4 : 1;          // scale vectors per ring slot: K blocks, or a tile's
+  static constexpr int SSLOTS = 4;               // ring slots
+  // FP8: registers move from the first eight warps to the epilogue's eight, which hold 64
+  // sums and 64 partials per thread: 512 threads launch with 128 each, 8 * 80 + 8 *
+  // 176 = 16 * 128 (no spills; at 72 and 184 the scale warps spilled).
+  static constexpr int CONTROL_REGS = 80, EPI_REGS = 176;
   static constexpr int PITCH = 80;               // bytes per token in a warp's store staging
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SC = OFF_B + STAGES * B_BYTES;
-  static constexpr int OFF_ST = OFF_SC + SRING * BT * 4;
+  static constexpr int OFF_ST = OFF_SC + SSLOTS * SV * BT * 4;
   static constexpr int OFF_LO = OFF_ST + NE * 16 * PITCH;
   static constexpr int OFF_CUM = OFF_LO + (kMaxExperts + 1) * 4;
   static constexpr int OFF_BAR = (OFF_CUM + (kMaxExperts + 1) * 4 + 7) & ~7;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NACC + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * NACC + 2 * SSLOTS + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int smem_bytes() { return 1024 + OFF_MISC + 16; }
   static_assert(1024 + OFF_MISC + 16 <= 232448, "shared memory");
-  static_assert(SRING >= 2 * NACC + 4, "scale ring, see the scale warp");
+  static_assert(!F8 || (EPI0 == 8 && THREADS == 512 && CONTROL_REGS + EPI_REGS <= 2 * 128),
+                "the register split stays within what the block launches with");
+  static_assert(!F8 || BT == 128, "FP8 epilogue: two groups of at most 64 columns");
 };
 
-// mbarrier wait without a suspend-time hint, bounded like wait_bounded, the same
-// answer in every lane.  The accumulators' round trip (MMA, commit, epilogue,
-// release, MMA) is made of such waits: with the 20 us hint of the other kernels
-// it took 8 % longer.
-__device__ __forceinline__ bool grouped_try_wait(uint32_t bar, uint32_t parity) {
+// mbarrier wait of the MMA issuer and its relay, bounded like wait_bounded, the same
+// answer in every lane.  No suspend-time hint: the accumulators' round trip (MMA,
+// commit, epilogue, release, MMA) took 8 % longer with the hint of the other waits.
+// The other roles keep it, since their polling takes issue slots from the epilogue.
+__device__ __forceinline__ bool prompt_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -100,42 +107,73 @@ __device__ __forceinline__ bool grouped_try_wait(uint32_t bar, uint32_t parity) 
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool grouped_wait_lane(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const uint32_t a = smem_u32(bar);
-  if (grouped_try_wait(a, parity)) return true;
-  const long long t0 = sm_cycles();
-  for (;;) {
-    if (grouped_try_wait(a, parity)) return true;
-    if (*abort_flag) return false;
-    if (sm_cycles() - t0 > kWaitLimitCycles) {
-      *abort_flag = 1;
-      atomicOr(&g_error_word, kErrTimeout);
-      return false;
+  bool ok = prompt_try_wait(a, parity);
+  if (!ok) {
+    const long long t0 = sm_cycles();
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = prompt_try_wait(a, parity);
+      if (ok || *abort_flag) break;
+      if (sm_cycles() - t0 > kWaitLimitCycles) {
+        *abort_flag = 1;
+        atomicOr(&g_error_word, kErrTimeout);
+        break;
+      }
     }
   }
+  return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ bool grouped_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, grouped_wait_lane(bar, parity, abort_flag));
+// Both phases complete.  The two polls overlap: the MMA warp's turn (polls, four MMAs,
+// commits) has to stay below the MMAs' own time, and two waits one after the other
+// did not.
+__device__ __forceinline__ bool prompt_wait2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1,
+                                             uint32_t parity1, volatile int* abort_flag) {
+  const bool a = prompt_try_wait(smem_u32(bar0), parity0), b = prompt_try_wait(smem_u32(bar1), parity1);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return prompt_wait(bar0, parity0, abort_flag) && prompt_wait(bar1, parity1, abort_flag);
 }
 
-// Asynchronous load of 16 columns of 16 tensor-memory lanes (taddr: lane 0 or 16 of
+// Asynchronous load of 32 columns of 16 tensor-memory lanes (taddr: lane 0 or 16 of
 // the warp's quadrant) as matrix fragments: lane l gets, for columns 8 i + 2 (l % 4)
 // and the next, rows l / 4 (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]).
 // A lane sees a quarter of the columns, so the per-token scales are four times fewer
 // reads than with one lane per channel.
-__device__ __forceinline__ void tmem_frag16_async(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                 "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
+__device__ __forceinline__ void tmem_frag32_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
-// Completes this thread's tensor-memory loads; r's values may be used after it.
-__device__ __forceinline__ void tmem_frag_wait(uint32_t (&r)[8], uint32_t (&s)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(s[0]), "+r"(s[1]), "+r"(s[2]), "+r"(s[3]), "+r"(s[4]), "+r"(s[5]),
-                 "+r"(s[6]), "+r"(s[7])::"memory");
+// 32 columns of all 32 lanes of the quadrant: v[h] rows 16 h ..
+__device__ __forceinline__ void tmem_frags_async(uint32_t taddr, uint32_t (&v)[2][16]) {
+  tmem_frag32_async(taddr, v[0]);
+  tmem_frag32_async(taddr + (16u << 16), v[1]);
+}
+// Completes this thread's tensor-memory loads; v's values may be used after it.
+__device__ __forceinline__ void tmem_frags_wait(uint32_t (&v)[2][16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)  // orders the uses after the wait
+      asm volatile(""
+                   : "+r"(v[h][i]), "+r"(v[h][i + 1]), "+r"(v[h][i + 2]), "+r"(v[h][i + 3]),
+                     "+r"(v[h][i + 4]), "+r"(v[h][i + 5]), "+r"(v[h][i + 6]), "+r"(v[h][i + 7]));
+}
+
+// Two fp32 fused multiply-adds, each rounded as fmaf: (a0, a1) * f + c.
+__device__ __forceinline__ uint64_t fma2(uint32_t a0, uint32_t a1, uint64_t f, uint64_t c) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\tfma.rn.f32x2 %0, a, %3, %4;\n\t}"
+      : "=l"(d)
+      : "r"(a0), "r"(a1), "l"(f), "l"(c));
+  return d;
 }
 
 // 2-D four-row gather load (rows r.x .. r.w of the tensor, 128 bytes each at
@@ -230,9 +268,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
   uint64_t* full = bars;                 // leader: pair's tiles of a stage have landed
   uint64_t* empty = bars + STAGES;       // both: the pair's MMAs are done with a stage
-  uint64_t* tfull = bars + 2 * STAGES;   // both: an accumulator (FP8: and its scales) is complete
-  uint64_t* tempty = tfull + NACC;       // leader: both epilogues released an accumulator
-  uint64_t* drain = tempty + NACC;
+  uint64_t* tfull = bars + 2 * STAGES;   // both: an accumulator is complete
+  uint64_t* tfree = tfull + NACC;        // both: this CTA's epilogue (leader: both CTAs') released one
+  uint64_t* sfull = tfree + NACC;        // both: a slot of the scale ring is written
+  uint64_t* sfree = sfull + Cfg::SSLOTS; // both: the epilogue is done with it
+  uint64_t* drain = sfree + Cfg::SSLOTS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
 
@@ -249,8 +289,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       mbar_init(empty + s, 1);
     }
     for (int a = 0; a < NACC; ++a) {
-      mbar_init(tfull + a, 2);
-      mbar_init(tempty + a, 2 * NE);
+      mbar_init(tfull + a, 1);
+      mbar_init(tfree + a, leader ? NE + 1 : NE);
+    }
+    for (int i = 0; i < Cfg::SSLOTS; ++i) {
+      mbar_init(sfull + i, 1);
+      mbar_init(sfree + i, NE);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -303,7 +347,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const int kbt = g.kb_total;
   griddep_launch_dependents();
 
-  if (warp == 0) {
+  if (warp < Cfg::EPI0) {
+   if constexpr (Cfg::F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::CONTROL_REGS));
+   if (warp == 0) {
     // ------------------------------- weights, and tokens in row order (TMA)
     if (lane == 0) {
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
@@ -321,7 +367,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
         const uint32_t bytes = 2 * (Cfg::A_BYTES + (g.rows ? half : 16 << box) * 128);
         for (int kb = 0; kb < kbt; ++kb) {
-          if (!grouped_wait_lane(empty + stage, phase ^ 1u, abort_flag)) {
+          if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
@@ -348,7 +394,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ----------------------------------------------- MMA issuer (leader)
+    // ------------------------------ MMA issuer (leader), relay (other CTA)
+    // The other CTA's releases of an accumulator reach the leader as one arrival: its
+    // epilogue warps arrive on their own CTA's barrier and this warp passes it on.
+    if (!leader) {
+      const uint32_t tfree_leader = mapa_shared(smem_u32(tfree), 0);
+      uint32_t local = 0;
+      bool ok = true;
+      for (int t = cluster; ok && t < num_tiles; t += nclusters)
+        for (int i = 0; i < (Cfg::F8 ? kbt : 1); ++i, ++local) {
+          const uint32_t a = local % NACC, u = local / NACC;
+          if (!prompt_wait(tfree + a, u & 1u, abort_flag)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_remote(tfree_leader + a * 8);
+          __syncwarp();
+        }
+    }
     if (leader) {
       GroupedWalk walk(lo, cum, g.tiles_n);
       uint32_t stage = 0, phase = 0, local = 0;
@@ -362,10 +422,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (Cfg::F8 || kb == 0) {  // a free accumulator: per K block (FP8) or per tile
             const uint32_t a = local % NACC, u = local / NACC;
             ++local;
-            if (!grouped_wait(tempty + a, (u & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+            ok = prompt_wait2(tfree + a, (u & 1u) ^ 1u, full + stage, phase, abort_flag);
             d = tmem + a * BT;
+          } else {
+            ok = prompt_wait(full + stage, phase, abort_flag);
           }
-          if (!grouped_wait(full + stage, phase, abort_flag)) { ok = false; break; }
+          if (!ok) break;
           tc_fence_after();
           const uint32_t sa = smem_u32(smA + stage * Cfg::A_BYTES);
           const uint32_t sb = smem_u32(smB + stage * Cfg::B_BYTES);
@@ -391,7 +453,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 3 && warp < Cfg::EPI0) {
+  } else if (warp >= 2 + Cfg::NS) {
     // ---------------------------------------------------- gathered tokens
     // Each lane fetches four rows of a stage; lane l of warp w takes rows 4 (NG l +
     // w) and up, so that the warps share the loads evenly.  A load takes its warp
@@ -400,7 +462,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // from eight 140 us.
     if (g.rows) {
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
-      const int j = (lane * Cfg::NG + warp - 3) * 4;
+      const int j = (lane * Cfg::NG + warp - 2 - Cfg::NS) * 4;
       GroupedWalk walk(lo, cum, g.tiles_n);
       uint32_t stage = 0, phase = 0;
       bool ok = true;
@@ -418,7 +480,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         int4 r4 = make_int4(g.M, g.M, g.M, g.M);
         if (mine) r4 = make_int4(token(0), token(1), token(2), token(3));
         for (int kb = 0; kb < kbt; ++kb) {
-          if (!grouped_wait(empty + stage, phase ^ 1u, abort_flag)) {
+          if (!warp_wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
@@ -433,27 +495,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
       }
     }
-  } else if (warp == 2) {
+  } else {
     // ------------------------------------------------------------- scales
-    // One vector per accumulator, in ring slot (its number) % SRING: INT8 s_tok of
-    // the tile's tokens, FP8 s_a[token, kb] * s_w[block, kb] (0 for rows outside).
-    // When accumulator n is published, n - NACC is known to be complete; its buffer
-    // had been released for it by an epilogue that was done with n - 2 NACC - 1.  So
-    // the slots still in use are those of n - 2 NACC .. n, and with SRING >= 2 NACC +
-    // 4 the four vectors before the next one to be published may be written.
-    constexpr int NV = BT / 32;  // 32-token vectors of a tile
+    // A ring slot holds SV vectors over the tile's tokens: INT8 the tile's s_tok; FP8 s_a *
+    // s_w of four K blocks (0 for rows outside).  FP8: two warps fill slots in turn,
+    // each with its next slot's loads in flight.  One warp that loaded, wrote and
+    // then loaded again gave four K blocks per L2 latency, and decode of 222
+    // rows over 64 experts (K = 1408, N = 2048) took 55 us.
+    constexpr int NV = BT / 32;
     GroupedWalk walk(lo, cum, g.tiles_n);
-    uint32_t local = 0;
+    uint32_t slot = 0, phase = 0;
+    const uint32_t mine = warp - 2;  // FP8: the slots of this parity
     bool ok = true;
-    // the accumulator's scales are in the ring; its barrier's previous use must be over
-    auto publish = [&]() {
-      const uint32_t a = local % NACC, u = local / NACC;
-      if (u > 0 && !grouped_wait(tfull + a, (u - 1u) & 1u, abort_flag)) return false;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tfull + a);
-      ++local;
-      return true;
-    };
     for (int t = cluster; ok && t < num_tiles; t += nclusters) {
       const GroupedTile tile = walk.at(t);
       int tok[NV];  // token of column 32 i + lane, -1: none
@@ -466,16 +519,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M)) tok[i] = r;
         }
       }
+      auto next_slot = [&]() {
+        if (++slot == Cfg::SSLOTS) { slot = 0; phase ^= 1u; }
+      };
       if constexpr (!Cfg::F8) {
-        float* slot = ring + (local % Cfg::SRING) * BT;
+        float v[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) slot[i * 32 + lane] = tok[i] >= 0 ? __ldg(g.s_a + tok[i]) : 0.0f;
-        ok = publish();
+        for (int i = 0; i < NV; ++i) v[i] = tok[i] >= 0 ? __ldg(g.s_a + tok[i]) : 0.0f;
+        if (!warp_wait_bounded(sfree + slot, phase ^ 1u, abort_flag)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) ring[slot * BT + i * 32 + lane] = v[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull + slot);
+        next_slot();
       } else {
         const int ch0 = tile.ct * 256 + static_cast<int>(rank) * 128;
         const float* sw = g.s_w + (static_cast<size_t>(tile.e) * (g.N >> 7) + (ch0 < g.N ? ch0 >> 7 : 0)) * kbt;
         const bool wide = (kbt & 3) == 0;  // a token's scales can be loaded four K blocks at a time
-        float4 v[NV], w;
         // scales of K blocks kb .. kb + 3 (0 past the last)
         auto load4 = [&](const float* p, int kb) {
           if (wide) return __ldg(reinterpret_cast<const float4*>(p + kb));
@@ -483,6 +543,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                              kb + 2 < kbt ? __ldg(p + kb + 2) : 0.0f,
                              kb + 3 < kbt ? __ldg(p + kb + 3) : 0.0f);
         };
+        float4 w, v[NV];
         auto fetch = [&](int kb) {
           w = load4(sw, kb);
 #pragma unroll
@@ -490,55 +551,43 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             v[i] = tok[i] >= 0 ? load4(g.s_a + static_cast<size_t>(tok[i]) * kbt, kb)
                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         };
-        uint32_t next = local;  // accumulator of the next vector to write
-        auto put = [&](float w_j, auto part) {
-          float* slot = ring + (next++ % Cfg::SRING) * BT;
+        int kb = (slot & 1u) == mine ? 0 : 4;  // this warp's first batch of the tile
+        if (kb < kbt) fetch(kb);
+        for (int b = 0; b < kbt; b += 4, next_slot()) {
+          if ((slot & 1u) != mine) continue;
+          if (!warp_wait_bounded(sfree + slot, phase ^ 1u, abort_flag)) { ok = false; break; }
+          float* to = ring + slot * (Cfg::SV * BT) + lane;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) slot[i * 32 + lane] = __fmul_rn(part(v[i]), w_j);
-        };
-        auto put_j = [&](int j) {
-          if (j == 0) put(w.x, [](const float4& f) { return f.x; });
-          else if (j == 1) put(w.y, [](const float4& f) { return f.y; });
-          else if (j == 2) put(w.z, [](const float4& f) { return f.z; });
-          else put(w.w, [](const float4& f) { return f.w; });
-        };
-        // four vectors ahead of the published ones, the loads of four more in flight
-        fetch(0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < kbt) put_j(j);
-        if (4 < kbt) fetch(4);
-        for (int kb = 0; ok && kb < kbt; kb += 4) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (ok && kb + j < kbt) {
-              ok = publish();
-              if (kb + 4 + j < kbt) put_j(j);
-            }
+          for (int i = 0; i < NV; ++i) {
+            to[i * 32] = __fmul_rn(v[i].x, w.x);
+            to[BT + i * 32] = __fmul_rn(v[i].y, w.y);
+            to[2 * BT + i * 32] = __fmul_rn(v[i].z, w.z);
+            to[3 * BT + i * 32] = __fmul_rn(v[i].w, w.w);
           }
-          if (kb + 8 < kbt) fetch(kb + 8);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfull + slot);
+          kb += 8;
+          if (kb < kbt) fetch(kb);
         }
       }
     }
+   }
   } else {
+    if constexpr (Cfg::F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::EPI_REGS));
     // ------------------------------------------------------------ epilogue
     const int ew = warp - Cfg::EPI0;
     const int q = warp & 3;                 // tensor-memory lane quadrant: 32 channels
     const int grp = ew >> 2;                // which columns of the tile
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t st = smem_u32(smem + Cfg::OFF_ST + ew * 16 * Cfg::PITCH);
-    const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
     const size_t N = static_cast<size_t>(g.N);
     auto release = [&](uint32_t a) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(tempty + a);
-        else mbar_arrive_remote(tempty_leader + a * 8);
-      }
+      if (lane == 0) mbar_arrive(tfree + a);
     };
     GroupedWalk walk(lo, cum, g.tiles_n);
-    uint32_t local = 0;
+    uint32_t local = 0, sslot = 0, sphase = 0;
     bool ok = true;
     for (int t = cluster; ok && t < num_tiles; t += nclusters) {
       const GroupedTile tile = walk.at(t);
@@ -554,21 +603,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           s_ch[k] = c < g.N ? __ldg(g.s_w + static_cast<size_t>(tile.e) * N + c) : 0.0f;
         }
         const uint32_t a = local % NACC, u = local / NACC;
-        const float* slot = ring + (local % Cfg::SRING) * BT;
+        const uint32_t r = local % Cfg::SSLOTS, ur = local / Cfg::SSLOTS;
+        const float* slot = ring + r * BT;
         ++local;
-        if (!grouped_wait(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
+        if (!warp_wait_bounded(sfull + r, ur & 1u, abort_flag) ||
+            !warp_wait_bounded(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t src = lanes + a * BT;
 #pragma unroll 1
         for (int c = grp * 32; c < n; c += (NE / 4) * 32) {
-          uint32_t v[2][2][8];  // [16 columns][16 channels]
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            tmem_frag16_async(src + c + i * 16, v[i][0]);
-            tmem_frag16_async(src + c + i * 16 + (16u << 16), v[i][1]);
-          }
-          tmem_frag_wait(v[0][0], v[0][1]);
-          tmem_frag_wait(v[1][0], v[1][1]);
+          uint32_t v[2][16];
+          tmem_frags_async(src + c, v);
+          tmem_frags_wait(v);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t pk[2][4];
@@ -577,7 +623,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               const float2 s = *reinterpret_cast<const float2*>(slot + c + i * 16 + b * 8 + (lane & 3) * 2);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const uint32_t* x = &v[i][k >> 1][4 * b + 2 * (k & 1)];
+                const uint32_t* x = &v[k >> 1][8 * i + 4 * b + 2 * (k & 1)];
                 pk[b][k] = pack_bf16x2(
                     __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(x[0])), s.x), s_ch[k]),
                     __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(x[1])), s.y), s_ch[k]));
@@ -588,59 +634,87 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         release(a);
+        if (lane == 0) mbar_arrive(sfree + r);
       } else {
-        // this warp's columns: a quarter of the tile's, in steps of 16
-        const int wcol = ((n >> 2) + 15) & ~15;
+        // this warp's columns: 64 or, of a tile of at most 64, 32; in two chunks of 32
+        const int wcol = n > 64 ? 64 : 32;
         const int col0 = grp * wcol;
-        const int ncol = max(0, min(wcol, n - col0));
-        constexpr int NC = Cfg::CPT / 16;
-        float acc[NC][2][8];
+        const bool has0 = col0 < n, has1 = wcol == 64 && col0 + 32 < n;
+        uint64_t acc[2][2][8];  // pairs of fp32 sums of neighbouring tokens
 #pragma unroll
-        for (int j = 0; j < NC * 16; ++j) (&acc[0][0][0])[j] = 0.0f;
+        for (int j = 0; j < 32; ++j) (&acc[0][0][0])[j] = 0;
+        uint32_t v[2][2][16];  // one chunk loads while the other is added
+        const uint32_t src = lanes + col0;
+        // acc += partials * scales of one chunk
+        auto add = [&](uint64_t (&x)[2][8], const uint32_t (&y)[2][16], const uint64_t (&f)[4]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int r = 2 * i; r < 2 * i + 2; ++r)
+                x[h][r] = fma2(y[h][2 * r], y[h][2 * r + 1], f[i], x[h][r]);
+        };
+        // A poll, a scale read and a tensor-memory read each take over 100 cycles even when
+        // everything is ready, so each is issued before the arithmetic that does not need
+        // it: the scales and the next K block's poll first, the second chunk's load before the
+        // first is added, the next K block's first before the second is added.
+        if (!prompt_wait(tfull + local % NACC, local / NACC & 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        if (has0) tmem_frags_async(src + local % NACC * BT, v[0]);
         for (int kb = 0; kb < kbt; ++kb, ++local) {
-          const uint32_t a = local % NACC, u = local / NACC;
-          if (!grouped_wait(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const float* slot = ring + (local % Cfg::SRING) * BT + col0 + (lane & 3) * 2;
-          const uint32_t src = lanes + a * BT + col0;
-          uint32_t v[NC][2][8];
+          const uint32_t a = local % NACC;
+          const uint32_t a1 = (local + 1) % NACC, p1 = (local + 1) / NACC & 1u;
+          if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) { ok = false; break; }
+          const float* s = ring + (sslot * Cfg::SV + (kb & 3)) * BT + col0 + (lane & 3) * 2;
+          uint64_t f[2][4];
 #pragma unroll
-          for (int i = 0; i < NC; ++i)
-            if (i * 16 < ncol) {
-              tmem_frag16_async(src + i * 16, v[i][0]);
-              tmem_frag16_async(src + i * 16 + (16u << 16), v[i][1]);
-            }
-#pragma unroll
-          for (int i = 0; i < NC; ++i) tmem_frag_wait(v[i][0], v[i][1]);
+          for (int i = 0; i < 4; ++i) {
+            f[0][i] = *reinterpret_cast<const uint64_t*>(s + i * 8);
+            f[1][i] = *reinterpret_cast<const uint64_t*>(s + 32 + i * 8);
+          }
+          const bool more = kb + 1 < kbt;
+          const bool polled = more && prompt_try_wait(smem_u32(tfull + a1), p1);
+          tmem_frags_wait(v[0]);
+          if (has1) {
+            tmem_frags_async(src + a * BT + 32, v[1]);
+            add(acc[0], v[0], f[0]);
+            tmem_frags_wait(v[1]);
+          }
           release(a);  // the K block is in registers
-#pragma unroll
-          for (int i = 0; i < NC; ++i)
-            if (i * 16 < ncol) {
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const float2 s = *reinterpret_cast<const float2*>(slot + i * 16 + b * 8);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                  for (int r = 0; r < 2; ++r) {
-                    float* x = &acc[i][h][4 * b + 2 * r];
-                    x[0] = __fmaf_rn(__uint_as_float(v[i][h][4 * b + 2 * r]), s.x, x[0]);
-                    x[1] = __fmaf_rn(__uint_as_float(v[i][h][4 * b + 2 * r + 1]), s.y, x[1]);
-                  }
-              }
+          const bool early = __all_sync(0xffffffffu, polled);
+          if (has1) {
+            if (early) {
+              tc_fence_after();
+              tmem_frags_async(src + a1 * BT, v[0]);
             }
+            add(acc[1], v[1], f[1]);
+          } else if (has0) {
+            add(acc[0], v[0], f[0]);
+          }
+          if ((kb & 3) == 3 || !more) {  // done with the slot's vectors
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sfree + sslot);
+            if (++sslot == Cfg::SSLOTS) { sslot = 0; sphase ^= 1u; }
+          }
+          if (more && !(early && has1)) {
+            if (!early && !prompt_wait(tfull + a1, p1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            if (has0) tmem_frags_async(src + a1 * BT, v[0]);
+          }
         }
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-          if (i * 16 < ncol) {
+        for (int i = 0; i < 4; ++i)
+          if (i < 2 ? has0 : has1) {
             uint32_t pk[2][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float* x = &acc[i][k >> 1][4 * b + 2 * (k & 1)];
-                pk[b][k] = pack_bf16x2(x[0], x[1]);
+                const uint64_t x = acc[i >> 1][k >> 1][4 * (i & 1) + 2 * b + (k & 1)];
+                pk[b][k] = pack_bf16x2(__uint_as_float(static_cast<uint32_t>(x)),
+                                       __uint_as_float(static_cast<uint32_t>(x >> 32)));
               }
             grouped_store<Cfg::PITCH>(st, out + (col0 + i * 16) * N, N, lane, pk,
                                       tile.nrows - col0 - i * 16, ch_ok);
