@@ -354,63 +354,27 @@ def fp8_block_mm(q_a, s_a, q_w, s_w):
     return y
 
 
-# ---- mixture-of-experts operators.  Tensors may be on any CUDA device: the launch
-# goes to theirs, on that device's current stream.  A decode step is a handful of
-# microseconds, so the checks are few attribute reads per tensor and the outputs are
-# made the cheapest way (empty_like and new_empty instead of empty with keywords).
+# ---- mixture-of-experts operators.  Their checks, allocations and calls are in the
+# extension _binding.so (csrc/binding.cpp).  Tensors may be on any CUDA device: the
+# launch goes to theirs, on that device's current stream.  A tensor of another type,
+# shape, layout or device raises ValueError; what the library refuses raises SqError.
 
-def _fits(t: torch.Tensor, dev: int, dtype: torch.dtype, shape) -> bool:
-    return (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous())
+_ext = None
 
 
-def _misfit(fn: str, dev: int, *wanted) -> ValueError:
-    """What is wrong with the first of (name, tensor or None, dtype, shape) that does not fit."""
-    if dev < 0:
-        return ValueError(f"{fn}: expected CUDA tensors")
-    for name, t, dtype, shape in wanted:
-        if t is not None and not _fits(t, dev, dtype, shape):
-            layout = "" if t.is_contiguous() else " (not contiguous)"
-            return ValueError(f"{fn}: {name} is {t.dtype} {list(t.shape)} on {t.device}{layout}, "
-                              f"expected contiguous {dtype} {list(shape)} on cuda:{dev}")
-    return ValueError(f"{fn}: unsupported arguments")
-
-
-def _launch(fn: str, dev: int, *args) -> None:
-    """Call the C entry point on the device's current stream, with it as the current device."""
-    f = getattr(lib(), fn)
-    if dev == torch._C._cuda_getDevice():
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if rc != 0:
-        raise SqError(fn, rc)
-
-
-def _dims(fn: str, name: str, t: torch.Tensor, dims: int):
-    if t.dim() != dims:
-        raise ValueError(f"{fn}: {name} has {t.dim()} dimensions, expected {dims}")
-    return t.shape
-
-
-def _add_rmsnorm(fn, h, residual, gamma, eps, mode, residual_out, code):
-    M, K = shape = _dims(fn, "h", h, 2)
-    dev, bf16, f32 = h.get_device(), torch.bfloat16, torch.float32
-    out = residual if residual_out is None else residual_out
-    if dev < 0 or not (_fits(h, dev, bf16, shape) and _fits(residual, dev, bf16, shape)
-                       and _fits(gamma, dev, f32, (K,)) and _fits(out, dev, bf16, shape)):
-        raise _misfit(fn, dev, ("h", h, bf16, shape), ("residual", residual, bf16, shape),
-                      ("gamma", gamma, f32, (K,)), ("residual_out", out, bf16, shape))
-    if residual_out is None:
-        out = torch.empty_like(h)
-    q = torch.empty_like(h, dtype=code)
-    per_row = mode == (0,) or mode == (K,) and K != 128
-    sc = gamma.new_empty(M) if per_row else gamma.new_empty((M, K // 128))
-    r = gamma.new_empty(M)
-    _launch(fn, dev, h.data_ptr(), residual.data_ptr(), gamma.data_ptr(), eps, *mode,
-            out.data_ptr(), q.data_ptr(), sc.data_ptr(), r.data_ptr(), M, K)
-    return out, q, sc, r
+def _extension():
+    """Load the extension; raises if it is missing."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _binding as ext
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(_HERE, '_binding.so')} cannot be loaded ({e}): build "
+                               "it with `python -m w8a8_int8_quantized_sq_b200.build`") from e
+        ext.set_errors(SqError, torch.OutOfMemoryError)
+        _ext = ext
+    return _ext
 
 
 def add_rmsnorm_quant(h, residual, gamma, eps: float, group: int = 0,
@@ -418,62 +382,23 @@ def add_rmsnorm_quant(h, residual, gamma, eps: float, group: int = 0,
     """residual' = h + residual (bf16), then RMSNorm + fold + INT8 quantisation of it:
     (residual', q, scales, inv_rms); group 0 = one scale per token, 128 = one per 128
     columns.  residual_out may be `residual` or `h` (in place)."""
-    return _add_rmsnorm("sq_add_rmsnorm_quant", h, residual, gamma, eps, (group,), residual_out,
-                        torch.int8)
+    return (_ext or _extension()).add_rmsnorm_quant(h, residual, gamma, eps, group, residual_out, False)
 
 
 def add_rmsnorm_quant_fp8(h, residual, gamma, eps: float,
                           residual_out: Optional[torch.Tensor] = None):
     """The same with E4M3 codes (uint8 bit patterns) and scales [M, K/128]."""
-    return _add_rmsnorm("sq_add_rmsnorm_quant_fp8", h, residual, gamma, eps, (), residual_out,
-                        torch.uint8)
-
-
-def _silu_mul(fn, gate_up, inv_s, mode, code):
-    T, K2 = _dims(fn, "gate_up", gate_up, 2)
-    K = K2 // 2
-    dev, bf16, f32 = gate_up.get_device(), torch.bfloat16, torch.float32
-    if dev < 0 or not (_fits(gate_up, dev, bf16, (T, 2 * K))
-                       and (inv_s is None or _fits(inv_s, dev, f32, (K,)))):
-        raise _misfit(fn, dev, ("gate_up", gate_up, bf16, (T, 2 * K)), ("inv_s", inv_s, f32, (K,)))
-    q = gate_up.new_empty((T, K), dtype=code)
-    sc = gate_up.new_empty((T,) if mode == (0,) or mode == (K,) and K != 128 else (T, K // 128),
-                           dtype=f32)
-    _launch(fn, dev, gate_up.data_ptr(), None if inv_s is None else inv_s.data_ptr(), *mode,
-            q.data_ptr(), sc.data_ptr(), T, K)
-    return q, sc
+    return (_ext or _extension()).add_rmsnorm_quant(h, residual, gamma, eps, 128, residual_out, True)
 
 
 def silu_mul_quant(gate_up, inv_s: Optional[torch.Tensor] = None, group: int = 0):
     """silu(gate) * up * inv_s of gate_up [T, 2K], INT8 quantised: (q, scales)."""
-    return _silu_mul("sq_silu_mul_quant", gate_up, inv_s, (group,), torch.int8)
+    return (_ext or _extension()).silu_mul_quant(gate_up, inv_s, group, False)
 
 
 def silu_mul_quant_fp8(gate_up, inv_s: Optional[torch.Tensor] = None):
     """The same with E4M3 codes (uint8 bit patterns) and scales [T, K/128]."""
-    return _silu_mul("sq_silu_mul_quant_fp8", gate_up, inv_s, (), torch.uint8)
-
-
-def _grouped(fn, q_a, s_a, q_w, s_w, offsets, rows, out, code):
-    M, K = _dims(fn, "q_a", q_a, 2)
-    E, N, _ = _dims(fn, "q_w", q_w, 3)
-    T = M if rows is None else rows.numel()
-    dev, bf16, f32, i32 = q_a.get_device(), torch.bfloat16, torch.float32, torch.int32
-    i8 = code is torch.int8
-    s_shape, w_shape = ((M,), (E, N)) if i8 else ((M, K // 128), (E, N // 128, K // 128))
-    if dev < 0 or not (
-            _fits(q_a, dev, code, (M, K)) and _fits(s_a, dev, f32, s_shape)
-            and _fits(q_w, dev, code, (E, N, K)) and _fits(s_w, dev, f32, w_shape)
-            and _fits(offsets, dev, i32, (E + 1,)) and (rows is None or _fits(rows, dev, i32, (T,)))
-            and (out is None or _fits(out, dev, bf16, (T, N)))):
-        raise _misfit(fn, dev, ("q_a", q_a, code, (M, K)), ("s_a", s_a, f32, s_shape),
-                      ("q_w", q_w, code, (E, N, K)), ("s_w", s_w, f32, w_shape),
-                      ("offsets", offsets, i32, (E + 1,)), ("rows", rows, i32, (T,)),
-                      ("out", out, bf16, (T, N)))
-    y = q_a.new_empty((T, N), dtype=bf16) if out is None else out
-    _launch(fn, dev, q_a.data_ptr(), s_a.data_ptr(), None if rows is None else rows.data_ptr(),
-            q_w.data_ptr(), s_w.data_ptr(), offsets.data_ptr(), y.data_ptr(), T, M, E, N, K)
-    return y
+    return (_ext or _extension()).silu_mul_quant(gate_up, inv_s, 128, True)
 
 
 def w8a8_grouped_mm(q_a, s_tok, q_w, s_ch, offsets, rows: Optional[torch.Tensor] = None,
@@ -481,13 +406,13 @@ def w8a8_grouped_mm(q_a, s_tok, q_w, s_ch, offsets, rows: Optional[torch.Tensor]
     """W8A8 products grouped by expert: row t (of expert e, offsets[e] <= t <
     offsets[e+1]) multiplies token rows[t] (None: token t) by q_w[e].  Rows outside the
     groups are left as they were in `out` (unspecified without it)."""
-    return _grouped("w8a8_grouped_mm", q_a, s_tok, q_w, s_ch, offsets, rows, out, torch.int8)
+    return (_ext or _extension()).grouped_mm(q_a, s_tok, q_w, s_ch, offsets, rows, out, False)
 
 
 def fp8_block_grouped_mm(q_a, s_a, q_w, s_w, offsets, rows: Optional[torch.Tensor] = None,
                          out: Optional[torch.Tensor] = None):
     """FP8 block-scaled products grouped by expert, rows as in w8a8_grouped_mm."""
-    return _grouped("fp8_block_grouped_mm", q_a, s_a, q_w, s_w, offsets, rows, out, torch.uint8)
+    return (_ext or _extension()).grouped_mm(q_a, s_a, q_w, s_w, offsets, rows, out, True)
 
 
 class PlanInfo(ctypes.Structure):

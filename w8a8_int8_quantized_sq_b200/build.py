@@ -1,4 +1,5 @@
-"""Build the sm_100a CUDA library libsqint8.so in this package directory.
+"""Build the sm_100a CUDA library libsqint8.so in this package directory, and the
+Python extension _binding.so that calls it for the mixture-of-experts operators.
 
 One translation unit (csrc/sqint8.cu) holds every kernel and the C ABI of
 include/sqint8.h.  Compiled with nvcc for sm_100a only, without fast math,
@@ -10,11 +11,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "sqint8.cu")
 LIB = os.path.join(HERE, "libsqint8.so")
+BINDING_SRC = os.path.join(HERE, "csrc", "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -24,22 +28,49 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std
 
 def sources():
     c = os.path.join(HERE, "csrc")
-    return [os.path.join(c, f) for f in os.listdir(c)] + [os.path.join(ROOT, "include", "sqint8.h")]
+    return [os.path.join(c, f) for f in os.listdir(c) if f != "binding.cpp"] + [
+        os.path.join(ROOT, "include", "sqint8.h")]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and all(
-            os.path.getmtime(LIB) >= os.path.getmtime(s) for s in sources()):
-        return LIB
-    cmd = [NVCC, *FLAGS, SRC, "-o", LIB + ".tmp"]
+def _fresh(target: str, inputs) -> bool:
+    return os.path.exists(target) and all(
+        os.path.getmtime(target) >= os.path.getmtime(s) for s in inputs)
+
+
+def _run(cmd, what: str, verbose: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libsqint8.so")
+        raise RuntimeError(f"building {what} failed")
     if verbose:
         sys.stderr.write(r.stderr)
-    os.replace(LIB + ".tmp", LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if force or not _fresh(LIB, sources()):
+        _run([NVCC, *FLAGS, SRC, "-o", LIB + ".tmp"], "libsqint8.so", verbose)
+        os.replace(LIB + ".tmp", LIB)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The extension needs PyTorch's headers and libsqint8.so (found beside it at run time)."""
+    header = os.path.join(ROOT, "include", "sqint8.h")
+    if not force and _fresh(BINDING, [BINDING_SRC, header]):
+        return BINDING
+    import torch
+    from torch.utils import cpp_extension
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], cuda]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-DNDEBUG", "-shared", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[a for i in includes for a in ("-isystem", i)], BINDING_SRC, "-o", BINDING + ".tmp",
+          "-L" + HERE, "-l:libsqint8.so", "-L" + lib_dir, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+          "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "_binding.so", verbose)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
