@@ -222,21 +222,23 @@ sq_status fp8_block_mm(const uint8_t* q_a, const float* s_a, const uint8_t* q_w,
 /* Mixture-of-experts operators ------------------------------------------ */
 
 /* Residual addition + RMSNorm + SmoothQuant fold + dynamic INT8 quantisation.
- * Per row m: residual_out = bf16_rne(f32(h) + f32(residual)) (one fp32 rounding,
- * one to bf16).  With x = residual_out: ss = sum_k f32(x)^2 accumulated in fp64
- * and rounded once to fp32; r = 1 / sqrt(ss * f32(1/K) + eps) and v_k = (f32(x_k)
- * * r) * gamma[k], each an IEEE fp32 operation; amax = max |v| over the row
- * (group == 0 or K: scales fp32 [M]) or over each 128 columns (group == 128:
- * scales fp32 [M, K/128]); scale = amax / 127, code = clamp(rint(v * f32(127 *
- * f32(1 / amax))), -127, 127), round-half-even; amax == 0 gives scale 0 and zero
- * codes.  (sq_rmsnorm_quant divides by K and by amax instead: a code next to a
- * rounding border may differ by one from its answer.)  h, residual, residual_out BF16 [M,K]; residual_out may be the
- * residual or h itself (in place); one that overlaps them otherwise is refused
- * (SQ_ERR_SHAPE).  inv_rms (fp32 [M], may be NULL) receives r.  eps > 0; K <= 24576.
- * The factor of the codes is held at the largest finite fp32 (amax below about
- * 3.7e-37).  A row that holds inf or NaN has unspecified codes and scales; the
- * other rows are not affected.  The launch may overlap the tail of any
- * preceding kernel (it reads and writes nothing before that kernel's end). */
+ * Per row m: x = residual_out = bf16_rne(f32(h) + f32(residual)) (one fp32
+ * rounding, one to bf16); ss = sum_k f32(x_k)^2 accumulated in fp64 and rounded
+ * once to fp32; r = 1 / sqrt(ss * f32(1/K) + eps) and v_k = (f32(x_k) * r) *
+ * gamma[k] (gamma from sq_fold_norm_weight), each an IEEE fp32 operation; amax =
+ * max |v| over the row (group == 0 or K: scales fp32 [M]) or over each 128 columns
+ * (group == 128: scales fp32 [M, K/128]); scale = f32(amax * f32(1/127)); code =
+ * clamp(rint(v * f32(127 * f32(1/amax))), -127, 127), round-half-even; amax == 0
+ * gives scale 0 and zero codes.  (sq_rmsnorm_quant divides by K, 127 and amax
+ * instead: its scales may differ in the last bits, and a code next to a rounding
+ * border by one.)  The factor 127 * f32(1/amax) is held at the largest finite
+ * fp32 (amax below about 3.7e-37).
+ * h, residual, residual_out BF16 [M,K]; residual_out may be the residual or h
+ * itself (in place); one that overlaps them otherwise is refused (SQ_ERR_SHAPE).
+ * inv_rms (fp32 [M], may be NULL) receives r.  eps > 0; K <= 24576.  A row that
+ * holds inf or NaN has unspecified codes and scales; the other rows are not
+ * affected.  The launch may overlap the tail of any preceding kernel (it reads
+ * and writes nothing before that kernel's end). */
 sq_status sq_add_rmsnorm_quant(const void* h_bf16, const void* residual_bf16, const float* gamma,
                                float eps, int64_t group, void* residual_out_bf16, int8_t* q_i8,
                                float* scales, float* inv_rms, int64_t M, int64_t K, void* stream);
