@@ -56,12 +56,17 @@ struct GroupedMaps {
   CUtensorMap m[4];
 };
 
-template <bool F8_>
+// BT: most tokens per tile.  256 (INT8, two accumulators for a tile each) and 128 (FP8,
+// four for a K block each) fill the tensor memory.  32 is for calls of at most 32 rows:
+// its token stages are small, so eleven weight stages fit instead of six and more of
+// the weights are on their way at once (a few tiles on a few SMs read no faster than
+// their rings are deep: 2 rows over 8 experts, K = N = 2048, 9.4 us with six).
+template <bool F8_, int BT_>
 struct GroupedCfg {
   static constexpr bool F8 = F8_;
-  static constexpr int BT = F8 ? 128 : 256;      // most tokens per tile
-  static constexpr int NACC = 512 / BT;          // accumulators (BT tensor-memory columns each)
-  static constexpr int STAGES = 6;
+  static constexpr int BT = BT_;
+  static constexpr int NACC = F8 ? 4 : 2;        // accumulators (BT tensor-memory columns each)
+  static constexpr int STAGES = BT == 32 ? 11 : F8 ? 8 : 6;
   static constexpr int A_BYTES = 128 * 128;      // weights staged by each CTA per K block
   static constexpr int B_BYTES = BT / 2 * 128;   // tokens staged by each CTA per K block, at most
   static constexpr int TMEM_COLS = 512;
@@ -89,7 +94,8 @@ struct GroupedCfg {
   static_assert(1024 + OFF_MISC + 16 <= 232448, "shared memory");
   static_assert(!F8 || (EPI0 == 8 && THREADS == 512 && CONTROL_REGS + EPI_REGS <= 2 * 128),
                 "the register split stays within what the block launches with");
-  static_assert(!F8 || BT == 128, "FP8 epilogue: two groups of at most 64 columns");
+  static_assert(NACC * BT <= 512, "tensor memory");
+  static_assert(!F8 || BT <= 128, "FP8 epilogue: two groups of at most 64 columns");
 };
 
 // mbarrier wait of the MMA issuer and its relay, bounded like wait_bounded, the same
@@ -202,21 +208,24 @@ struct GroupedWalk {
   int tiles_n, e;
   __device__ __forceinline__ GroupedWalk(const int* lo_, const int* cum_, int tiles_n_)
       : lo(lo_), cum(cum_), tiles_n(tiles_n_), e(0) {}
-  // rows per token tile of an expert with r rows in nt tiles (at most BT)
-  static __device__ __forceinline__ int width(int r, int nt) { return ((r + nt - 1) / nt + 31) & ~31; }
   // tile t; t must not decrease from call to call
   __device__ __forceinline__ GroupedTile at(int t) {
     while (t >= cum[e + 1] * tiles_n) ++e;
     const int nt = cum[e + 1] - cum[e];
     const int i = t - cum[e] * tiles_n;
     const int r = lo[e + 1] - lo[e];
-    const int w = width(r, nt);
     GroupedTile g;
     g.e = e;
-    g.ct = i / nt;
-    const int tt = i - g.ct * nt;
-    g.row0 = lo[e] + tt * w;
-    g.nrows = min(w, r - tt * w);
+    g.ct = i;
+    g.row0 = lo[e];
+    g.nrows = r;
+    if (nt > 1) {  // the divisions take a few hundred cycles, which short tiles would notice
+      const int w = ((r + nt - 1) / nt + 31) & ~31;  // rows per token tile, at most BT
+      g.ct = i / nt;
+      const int tt = i - g.ct * nt;
+      g.row0 += tt * w;
+      g.nrows = min(w, r - tt * w);
+    }
     return g;
   }
 };
@@ -591,9 +600,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     bool ok = true;
     for (int t = cluster; ok && t < num_tiles; t += nclusters) {
       const GroupedTile tile = walk.at(t);
+      const int n = (tile.nrows + 31) & ~31;
       const int ch = tile.ct * 256 + static_cast<int>(rank) * 128 + q * 32;  // this warp's channels
       const bool ch_ok = ch + (lane & 3) * 8 < g.N;
-      const int n = (tile.nrows + 31) & ~31;
       __nv_bfloat16* out = g.out + static_cast<size_t>(tile.row0) * N + ch;
       if constexpr (!Cfg::F8) {
         float s_ch[4];  // of channels 8 k + lane / 4
@@ -656,51 +665,65 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 x[h][r] = fma2(y[h][2 * r], y[h][2 * r + 1], f[i], x[h][r]);
         };
         // A poll, a scale read and a tensor-memory read each take over 100 cycles even when
-        // everything is ready, so each is issued before the arithmetic that does not need
-        // it: the scales and the next K block's poll first, the second chunk's load before the
-        // first is added, the next K block's first before the second is added.
-        if (!prompt_wait(tfull + local % NACC, local / NACC & 1u, abort_flag)) { ok = false; break; }
+        // everything is ready, so K blocks are taken in pairs on one poll (commits arrive in
+        // order: the second is complete after the first), and each read is issued
+        // before the arithmetic that does not need it: the second chunk's load before the
+        // first is added, the next block's first before the second is added.
+        auto load_scales = [&](uint64_t (&f)[4], int kb, int c) {
+          const float* s = ring + (sslot * Cfg::SV + (kb & 3)) * BT + col0 + c + (lane & 3) * 2;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const uint64_t*>(s + i * 8);
+        };
+        const uint32_t l1 = local + (kbt > 1 ? 1 : 0);
+        if (!prompt_wait(tfull + l1 % NACC, l1 / NACC & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (has0) tmem_frags_async(src + local % NACC * BT, v[0]);
-        for (int kb = 0; kb < kbt; ++kb, ++local) {
-          const uint32_t a = local % NACC;
-          const uint32_t a1 = (local + 1) % NACC, p1 = (local + 1) / NACC & 1u;
-          if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) { ok = false; break; }
-          const float* s = ring + (sslot * Cfg::SV + (kb & 3)) * BT + col0 + (lane & 3) * 2;
-          uint64_t f[2][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[0][i] = *reinterpret_cast<const uint64_t*>(s + i * 8);
-            f[1][i] = *reinterpret_cast<const uint64_t*>(s + 32 + i * 8);
-          }
-          const bool more = kb + 1 < kbt;
-          const bool polled = more && prompt_try_wait(smem_u32(tfull + a1), p1);
+        if (has1) tmem_frags_async(src + local % NACC * BT + 32, v[1]);
+        uint64_t f[2][4] = {};
+        // One K block whose first chunk is in flight; `load_next` may request the next
+        // block's first chunk (into v[0]) once this one's is used.
+        auto block = [&](uint32_t a, int kb, auto&& load_next) {
           tmem_frags_wait(v[0]);
-          if (has1) {
-            tmem_frags_async(src + a * BT + 32, v[1]);
-            add(acc[0], v[0], f[0]);
-            tmem_frags_wait(v[1]);
-          }
-          release(a);  // the K block is in registers
-          const bool early = __all_sync(0xffffffffu, polled);
-          if (has1) {
+          tmem_frags_wait(v[1]);
+          release(a);
+          if (has0) add(acc[0], v[0], f[0]);
+          if (has1) add(acc[1], v[1], f[1]);
+          load_next();
+        };
+        for (int kb = 0; kb < kbt; kb += 2) {
+          if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) { ok = false; break; }
+          load_scales(f[0], kb, 0);
+          if constexpr (BT > 32) load_scales(f[1], kb, 32);
+          const bool two = kb + 1 < kbt, more = kb + 2 < kbt;
+          const uint32_t a = local % NACC, a1 = (local + 1) % NACC;
+          const uint32_t l2 = local + 2, l3 = kb + 3 < kbt ? local + 3 : l2;  // the next pair
+          const bool polled = more && prompt_try_wait(smem_u32(tfull + l3 % NACC), l3 / NACC & 1u);
+          bool early = false;
+          auto next_pair = [&]() {
+            early = __all_sync(0xffffffffu, polled);
             if (early) {
               tc_fence_after();
-              tmem_frags_async(src + a1 * BT, v[0]);
+              { if (has0) tmem_frags_async(src + l2 % NACC * BT, v[0]); if (has1) tmem_frags_async(src + l2 % NACC * BT + 32, v[1]); }
             }
-            add(acc[1], v[1], f[1]);
-          } else if (has0) {
-            add(acc[0], v[0], f[0]);
+          };
+          if (two) {
+            block(a, kb, [&]() { { if (has0) tmem_frags_async(src + a1 * BT, v[0]); if (has1) tmem_frags_async(src + a1 * BT + 32, v[1]); } });
+            load_scales(f[0], kb + 1, 0);
+            if constexpr (BT > 32) load_scales(f[1], kb + 1, 32);
+            block(a1, kb + 1, next_pair);
+          } else {
+            block(a, kb, next_pair);
           }
-          if ((kb & 3) == 3 || !more) {  // done with the slot's vectors
+          if ((kb & 2) || !more) {  // done with the slot's vectors
             __syncwarp();
             if (lane == 0) mbar_arrive(sfree + sslot);
             if (++sslot == Cfg::SSLOTS) { sslot = 0; sphase ^= 1u; }
           }
-          if (more && !(early && has1)) {
-            if (!early && !prompt_wait(tfull + a1, p1, abort_flag)) { ok = false; break; }
+          local += two ? 2 : 1;
+          if (more && !early) {
+            if (!prompt_wait(tfull + l3 % NACC, l3 / NACC & 1u, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            if (has0) tmem_frags_async(src + a1 * BT, v[0]);
+            { if (has0) tmem_frags_async(src + l2 % NACC * BT, v[0]); if (has1) tmem_frags_async(src + l2 % NACC * BT + 32, v[1]); }
           }
         }
         if (!ok) break;

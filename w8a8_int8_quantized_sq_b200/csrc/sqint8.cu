@@ -801,11 +801,10 @@ sq_status silu_mul_quant(const void* gate_up, const float* inv_smooth, int fmt, 
   return row_quant<RQ_SILU>(fmt, a, static_cast<cudaStream_t>(stream));
 }
 
-template <bool F8>
+template <class Cfg>
 sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows, const void* q_w,
                          const float* s_w, const int32_t* offsets, void* y, int64_t T, int64_t M,
                          int64_t E, int64_t N, int64_t K, cudaStream_t st) {
-  using Cfg = GroupedCfg<F8>;
   const uint64_t k = static_cast<uint64_t>(K);
   CUtensorMap tw;
   GroupedMaps tx{};
@@ -881,8 +880,9 @@ sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* 
       !aligned16(offsets) || !aligned16(y) || (rows && !aligned16(rows)))
     return SQ_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return f8 ? launch_grouped<true>(q_a, s_a, rows, q_w, s_w, offsets, y, T, M, E, N, K, st)
-            : launch_grouped<false>(q_a, s_a, rows, q_w, s_w, offsets, y, T, M, E, N, K, st);
+  auto launch = f8 ? (T <= 32 ? launch_grouped<GroupedCfg<true, 32>> : launch_grouped<GroupedCfg<true, 128>>)
+                   : (T <= 32 ? launch_grouped<GroupedCfg<false, 32>> : launch_grouped<GroupedCfg<false, 256>>);
+  return launch(q_a, s_a, rows, q_w, s_w, offsets, y, T, M, E, N, K, st);
 }
 
 }  // namespace
