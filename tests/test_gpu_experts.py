@@ -94,6 +94,17 @@ def test_grouped_i8_bit_exact(counts, N, K, gather):
     sq.check_device_error()
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N,K", [(16, 512), (272, 1152), (1536, 2176), (5120, 640)])
+@pytest.mark.parametrize("counts", [[1], [0, 0, 2], [3, 0, 29], [1] * 32])
+def test_grouped_i8_few_rows(counts, N, K, gather):
+    """Calls of at most 32 rows, whose tiles may share K among the pairs of a cluster."""
+    c = i8_case(counts, N, K, gather, 12 + N + len(counts))
+    y = sq.w8a8_grouped_mm(*cuda(*c[:5]), rows=cuda(c[5])[0])
+    assert_bits(y, i8_reference(*c, torch.zeros(sum(counts), N, dtype=torch.bfloat16)), "y")
+    sq.check_device_error()
+
+
 def test_grouped_i8_many_tiles():
     """More tiles than CTA pairs, groups of several token tiles, a long K."""
     g = gen(5)
@@ -207,12 +218,31 @@ def check_fp8(y, c, what):
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("counts,N,K", [([1], 128, 128), ([0, 5, 33], 128, 384),
                                         ([70, 0, 300, 130], 384, 1408), ([9] * 20, 256, 256),
-                                        ([200, 520], 640, 640)])
+                                        ([200, 520], 640, 640), ([1], 256, 512), ([0, 3, 0, 29], 384, 1152),
+                                        ([2], 1536, 2176), ([1] * 32, 640, 640), ([32], 128, 1664)])
 def test_grouped_fp8(counts, N, K, gather):
     c = fp8_case(counts, N, K, gather, 51 + N + K)
     y = sq.fp8_block_grouped_mm(*cuda(*c[:5]), rows=cuda(c[5])[0])
     check_fp8(y, c, f"counts {counts} N {N} K {K}")
     sq.check_device_error()
+
+
+@pytest.mark.parametrize("kind", ["i8", "fp8"])
+def test_grouped_answers_do_not_depend_on_timing(kind):
+    """The same call many times, alone and under load on another stream: the same bits."""
+    c = (i8_case if kind == "i8" else fp8_case)([2, 0, 7], 640, 2176, True, 62)
+    mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+    args, rows = cuda(*c[:5]), cuda(c[5])[0]
+    want = mm(*args, rows=rows)
+    load = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            load @ load
+    got = [mm(*args, rows=rows) for _ in range(50)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, g) for g in got)
 
 
 def test_grouped_fp8_equals_the_dense_product():

@@ -45,6 +45,7 @@ struct GroupedArgs {
   int T, M, E, N;
   int kb_total;            // K / 128
   int tiles_n;             // ceil(N / 256)
+  int split;               // CTA pairs that share a tile's K (1 unless the tiles are 32 tokens wide)
 };
 
 // Tensor maps of the token rows: boxes of 16, 32, 64 and 128 rows, of which a tile
@@ -57,16 +58,19 @@ struct GroupedMaps {
 };
 
 // BT: most tokens per tile.  256 (INT8, two accumulators for a tile each) and 128 (FP8,
-// four for a K block each) fill the tensor memory.  32 is for calls of at most 32 rows:
-// its token stages are small, so eleven weight stages fit instead of six and more of
-// the weights are on their way at once (a few tiles on a few SMs read no faster than
-// their rings are deep: 2 rows over 8 experts, K = N = 2048, 9.4 us with six).
+// four for a K block each) fill the tensor memory.  32 is for calls of at most 32 rows,
+// whose few tiles would leave most SMs idle (an SM pair reads about 100 bytes/ns, and
+// a deeper ring does not change that): there a tile's K may be split over the 2 or 4
+// CTA pairs of one cluster.  The other pairs' partial sums meet in the first's shared
+// memory and are added in the order of K, so the answer does not depend on timing.
 template <bool F8_, int BT_>
 struct GroupedCfg {
   static constexpr bool F8 = F8_;
   static constexpr int BT = BT_;
   static constexpr int NACC = F8 ? 4 : 2;        // accumulators (BT tensor-memory columns each)
-  static constexpr int STAGES = BT == 32 ? 11 : F8 ? 8 : 6;
+  static constexpr bool SPLIT = BT == 32;        // K may be split over the cluster's pairs
+  static constexpr int STAGES = BT == 32 || F8 ? 8 : 6;
+  static constexpr int PART_BYTES = 128 * 32 * 4;  // one CTA's partial sums of a split tile
   static constexpr int A_BYTES = 128 * 128;      // weights staged by each CTA per K block
   static constexpr int B_BYTES = BT / 2 * 128;   // tokens staged by each CTA per K block, at most
   static constexpr int TMEM_COLS = 512;
@@ -85,10 +89,11 @@ struct GroupedCfg {
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SC = OFF_B + STAGES * B_BYTES;
   static constexpr int OFF_ST = OFF_SC + SSLOTS * SV * BT * 4;
-  static constexpr int OFF_LO = OFF_ST + NE * 16 * PITCH;
+  static constexpr int OFF_PART = OFF_ST + NE * 16 * PITCH;
+  static constexpr int OFF_LO = OFF_PART + (SPLIT ? 3 * PART_BYTES : 0);
   static constexpr int OFF_CUM = OFF_LO + (kMaxExperts + 1) * 4;
   static constexpr int OFF_BAR = (OFF_CUM + (kMaxExperts + 1) * 4 + 7) & ~7;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * NACC + 2 * SSLOTS + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * NACC + 2 * SSLOTS + 4;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int smem_bytes() { return 1024 + OFF_MISC + 16; }
   static_assert(1024 + OFF_MISC + 16 <= 232448, "shared memory");
@@ -180,6 +185,17 @@ __device__ __forceinline__ uint64_t fma2(uint32_t a0, uint32_t a1, uint64_t f, u
       : "=l"(d)
       : "r"(a0), "r"(a1), "l"(f), "l"(c));
   return d;
+}
+
+// Arrive (once the pair's MMAs issued so far are done) on the mbarrier at this offset in
+// both CTAs of the pair led by cluster rank `lead`.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tcvt.u16.u32 m, %1;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], m;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(3u << lead)
+      : "memory");
 }
 
 // 2-D four-row gather load (rows r.x .. r.w of the tensor, 128 bytes each at
@@ -281,16 +297,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   uint64_t* tfree = tfull + NACC;        // both: this CTA's epilogue (leader: both CTAs') released one
   uint64_t* sfull = tfree + NACC;        // both: a slot of the scale ring is written
   uint64_t* sfree = sfull + Cfg::SSLOTS; // both: the epilogue is done with it
-  uint64_t* drain = sfree + Cfg::SSLOTS;
+  uint64_t* pfull = sfree + Cfg::SSLOTS; // first pair: another pair's partial sums have arrived
+  uint64_t* drain = pfull + 3;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1u;      // within the CTA pair
+  const uint32_t lead = crank & ~1u;     // the pair's leader
   const bool leader = rank == 0;
-  const int cluster = blockIdx.x >> 1;
-  const int nclusters = gridDim.x >> 1;
+  const int split = Cfg::SPLIT ? g.split : 1;
+  const int pair = Cfg::SPLIT ? static_cast<int>(crank >> 1) : 0;
+  const int cluster = blockIdx.x / (2 * split);
+  const int nclusters = gridDim.x / (2 * split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -305,6 +326,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       mbar_init(sfull + i, 1);
       mbar_init(sfree + i, NE);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(pfull + i, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -354,6 +376,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const uint32_t tmem = *tmem_holder;
   const int num_tiles = cum[g.E] * g.tiles_n;
   const int kbt = g.kb_total;
+  // this pair's K blocks: nk of them from k0
+  const int k0 = Cfg::SPLIT ? kbt * pair / split : 0;
+  const int nk = Cfg::SPLIT ? kbt * (pair + 1) / split - k0 : kbt;
   griddep_launch_dependents();
 
   if (warp < Cfg::EPI0) {
@@ -361,7 +386,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
    if (warp == 0) {
     // ------------------------------- weights, and tokens in row order (TMA)
     if (lane == 0) {
-      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+      const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
       const uint64_t pol = policy_evict_normal();
       GroupedWalk walk(lo, cum, g.tiles_n);
       uint32_t stage = 0, phase = 0;
@@ -375,16 +400,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // the smallest box of 16 << box rows that holds the half
         const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
         const uint32_t bytes = 2 * (Cfg::A_BYTES + (g.rows ? half : 16 << box) * 128);
-        for (int kb = 0; kb < kbt; ++kb) {
+        for (int kb = 0; kb < nk; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
           if (leader) mbar_arrive_expect_tx(full + stage, bytes);
-          tma_load_2d_pair(smA + stage * Cfg::A_BYTES, &tmW, kb * 128, w_row,
+          tma_load_2d_pair(smA + stage * Cfg::A_BYTES, &tmW, (k0 + kb) * 128, w_row,
                            full_leader + stage * 8, pol);
           if (!g.rows)
-            tma_load_2d_pair(smB + stage * Cfg::B_BYTES, &tmX.m[box], kb * 128, x_row,
+            tma_load_2d_pair(smB + stage * Cfg::B_BYTES, &tmX.m[box], (k0 + kb) * 128, x_row,
                              full_leader + stage * 8, pol);
           ++fills;
           if (++stage == STAGES) {
@@ -407,11 +432,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // The other CTA's releases of an accumulator reach the leader as one arrival: its
     // epilogue warps arrive on their own CTA's barrier and this warp passes it on.
     if (!leader) {
-      const uint32_t tfree_leader = mapa_shared(smem_u32(tfree), 0);
+      const uint32_t tfree_leader = mapa_shared(smem_u32(tfree), lead);
       uint32_t local = 0;
       bool ok = true;
       for (int t = cluster; ok && t < num_tiles; t += nclusters)
-        for (int i = 0; i < (Cfg::F8 ? kbt : 1); ++i, ++local) {
+        for (int i = 0; i < (Cfg::F8 ? nk : 1); ++i, ++local) {
           const uint32_t a = local % NACC, u = local / NACC;
           if (!prompt_wait(tfree + a, u & 1u, abort_flag)) { ok = false; break; }
           if (lane == 0) mbar_arrive_remote(tfree_leader + a * 8);
@@ -427,7 +452,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int n = (tile.nrows + 31) & ~31;
         const uint32_t idesc = Cfg::F8 ? idesc_e4m3_f32_m256(n) : idesc_i8_s32_m256(n);
         uint32_t d = 0;
-        for (int kb = 0; kb < kbt; ++kb) {
+        for (int kb = 0; kb < nk; ++kb) {
           if (Cfg::F8 || kb == 0) {  // a free accumulator: per K block (FP8) or per tile
             const uint32_t a = local % NACC, u = local / NACC;
             ++local;
@@ -449,8 +474,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               else
                 mma_i8_pair(d, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32), idesc, acc);
             }
-            mma_commit_pair_both(empty + stage);
-            if (Cfg::F8 || kb == kbt - 1) mma_commit_pair_both(tfull + (local - 1) % NACC);
+            commit_pair(empty + stage, lead);
+            if (Cfg::F8 || kb == nk - 1) commit_pair(tfull + (local - 1) % NACC, lead);
           }
           __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -470,7 +495,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // 32768 rows over 64 experts, K = N = 2048, take 346 us, from four 152 us,
     // from eight 140 us.
     if (g.rows) {
-      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+      const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
       const int j = (lane * Cfg::NG + warp - 2 - Cfg::NS) * 4;
       GroupedWalk walk(lo, cum, g.tiles_n);
       uint32_t stage = 0, phase = 0;
@@ -488,13 +513,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const bool mine = j < half;
         int4 r4 = make_int4(g.M, g.M, g.M, g.M);
         if (mine) r4 = make_int4(token(0), token(1), token(2), token(3));
-        for (int kb = 0; kb < kbt; ++kb) {
+        for (int kb = 0; kb < nk; ++kb) {
           if (!warp_wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
           if (mine)
-            tma_gather4_pair(smB + stage * Cfg::B_BYTES + j * 128, &tmX.m[0], kb * 128, r4,
+            tma_gather4_pair(smB + stage * Cfg::B_BYTES + j * 128, &tmX.m[0], (k0 + kb) * 128, r4,
                              full_leader + stage * 8);
           __syncwarp();
           if (++stage == STAGES) {
@@ -543,26 +568,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         next_slot();
       } else {
         const int ch0 = tile.ct * 256 + static_cast<int>(rank) * 128;
-        const float* sw = g.s_w + (static_cast<size_t>(tile.e) * (g.N >> 7) + (ch0 < g.N ? ch0 >> 7 : 0)) * kbt;
-        const bool wide = (kbt & 3) == 0;  // a token's scales can be loaded four K blocks at a time
+        const float* sw = g.s_w + (static_cast<size_t>(tile.e) * (g.N >> 7) + (ch0 < g.N ? ch0 >> 7 : 0)) * kbt + k0;
+        const bool wide = ((kbt | k0) & 3) == 0;  // a token's scales can be loaded four K blocks at a time
         // scales of K blocks kb .. kb + 3 (0 past the last)
         auto load4 = [&](const float* p, int kb) {
           if (wide) return __ldg(reinterpret_cast<const float4*>(p + kb));
-          return make_float4(__ldg(p + kb), kb + 1 < kbt ? __ldg(p + kb + 1) : 0.0f,
-                             kb + 2 < kbt ? __ldg(p + kb + 2) : 0.0f,
-                             kb + 3 < kbt ? __ldg(p + kb + 3) : 0.0f);
+          return make_float4(__ldg(p + kb), kb + 1 < nk ? __ldg(p + kb + 1) : 0.0f,
+                             kb + 2 < nk ? __ldg(p + kb + 2) : 0.0f,
+                             kb + 3 < nk ? __ldg(p + kb + 3) : 0.0f);
         };
         float4 w, v[NV];
         auto fetch = [&](int kb) {
           w = load4(sw, kb);
 #pragma unroll
           for (int i = 0; i < NV; ++i)
-            v[i] = tok[i] >= 0 ? load4(g.s_a + static_cast<size_t>(tok[i]) * kbt, kb)
+            v[i] = tok[i] >= 0 ? load4(g.s_a + static_cast<size_t>(tok[i]) * kbt + k0, kb)
                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         };
         int kb = (slot & 1u) == mine ? 0 : 4;  // this warp's first batch of the tile
-        if (kb < kbt) fetch(kb);
-        for (int b = 0; b < kbt; b += 4, next_slot()) {
+        if (kb < nk) fetch(kb);
+        for (int b = 0; b < nk; b += 4, next_slot()) {
           if ((slot & 1u) != mine) continue;
           if (!warp_wait_bounded(sfree + slot, phase ^ 1u, abort_flag)) { ok = false; break; }
           float* to = ring + slot * (Cfg::SV * BT) + lane;
@@ -576,7 +601,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(sfull + slot);
           kb += 8;
-          if (kb < kbt) fetch(kb);
+          if (kb < nk) fetch(kb);
         }
       }
     }
@@ -594,6 +619,33 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tfree + a);
+    };
+    // Split tiles: the other pairs hand their 32 values per thread to the same thread of
+    // the first pair, which adds them in the order of the pairs (a cluster has at
+    // most one tile then, so no buffer is used twice).  False: a wait gave up.
+    auto combine = [&](auto&& value, auto&& add) {
+      uint8_t* mine = smem + Cfg::OFF_PART + q * 4096 + lane * 16;
+      if (pair > 0) {
+        const uint32_t to = mapa_shared(smem_u32(mine) + (pair - 1) * Cfg::PART_BYTES, rank);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_cluster_v4(to + i * 512, value(4 * i), value(4 * i + 1), value(4 * i + 2), value(4 * i + 3));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(pfull + pair - 1), rank));
+        return true;
+      }
+      for (int p = 0; p < split - 1; ++p) {
+        if (!__all_sync(0xffffffffu, wait_bounded_cluster(pfull + p, 0, abort_flag))) return false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(mine + p * Cfg::PART_BYTES + i * 512);
+          add(4 * i, x.x);
+          add(4 * i + 1, x.y);
+          add(4 * i + 2, x.z);
+          add(4 * i + 3, x.w);
+        }
+      }
+      return true;
     };
     GroupedWalk walk(lo, cum, g.tiles_n);
     uint32_t local = 0, sslot = 0, sphase = 0;
@@ -624,6 +676,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           uint32_t v[2][16];
           tmem_frags_async(src + c, v);
           tmem_frags_wait(v);
+          if constexpr (Cfg::SPLIT) {
+            if (split > 1) {
+              ok = combine([&](int i) { return v[i >> 4][i & 15]; },
+                           [&](int i, uint32_t x) { v[i >> 4][i & 15] += x; });
+              if (pair > 0 || !ok) break;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t pk[2][4];
@@ -674,7 +733,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const uint64_t*>(s + i * 8);
         };
-        const uint32_t l1 = local + (kbt > 1 ? 1 : 0);
+        const uint32_t l1 = local + (nk > 1 ? 1 : 0);
         if (!prompt_wait(tfull + l1 % NACC, l1 / NACC & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (has0) tmem_frags_async(src + local % NACC * BT, v[0]);
@@ -690,13 +749,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (has1) add(acc[1], v[1], f[1]);
           load_next();
         };
-        for (int kb = 0; kb < kbt; kb += 2) {
+        for (int kb = 0; kb < nk; kb += 2) {
           if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) { ok = false; break; }
           load_scales(f[0], kb, 0);
           if constexpr (BT > 32) load_scales(f[1], kb, 32);
-          const bool two = kb + 1 < kbt, more = kb + 2 < kbt;
+          const bool two = kb + 1 < nk, more = kb + 2 < nk;
           const uint32_t a = local % NACC, a1 = (local + 1) % NACC;
-          const uint32_t l2 = local + 2, l3 = kb + 3 < kbt ? local + 3 : l2;  // the next pair
+          const uint32_t l2 = local + 2, l3 = kb + 3 < nk ? local + 3 : l2;  // the next pair
           const bool polled = more && prompt_try_wait(smem_u32(tfull + l3 % NACC), l3 / NACC & 1u);
           bool early = false;
           auto next_pair = [&]() {
@@ -727,6 +786,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         if (!ok) break;
+        if constexpr (Cfg::SPLIT) {
+          if (split > 1 && has0) {
+            float sum[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              sum[i] = __uint_as_float(static_cast<uint32_t>(acc[0][i >> 4][(i >> 1) & 7] >> (32 * (i & 1))));
+            ok = combine([&](int i) { return __float_as_uint(sum[i]); },
+                         [&](int i, uint32_t x) { sum[i] = __fadd_rn(sum[i], __uint_as_float(x)); });
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[0][i >> 3][i & 7] = static_cast<uint64_t>(__float_as_uint(sum[2 * i + 1])) << 32 |
+                                      __float_as_uint(sum[2 * i]);
+            if (pair > 0 || !ok) break;  // the cluster's only tile
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (i < 2 ? has0 : has1) {

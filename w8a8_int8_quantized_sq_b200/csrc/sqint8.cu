@@ -801,6 +801,35 @@ sq_status silu_mul_quant(const void* gate_up, const float* inv_smooth, int fmt, 
   return row_quant<RQ_SILU>(fmt, a, static_cast<cudaStream_t>(stream));
 }
 
+// Clusters of `split` CTA pairs that the device holds at once (asked once per device),
+// 0 if it cannot be told.
+template <class Cfg>
+int grouped_clusters(int split, int smem) {
+  static std::atomic<int> cap[64][3];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& slot = cap[dev][split / 2];
+  int mc = slot.load(std::memory_order_acquire);
+  if (mc > 0) return mc;
+  if (cudaFuncSetAttribute(grouped_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * split);
+  cfg.blockDim = dim3(Cfg::THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&mc, grouped_kernel<Cfg>, &cfg) != cudaSuccess || mc <= 0) return 0;
+  slot.store(mc, std::memory_order_release);
+  return mc;
+}
+
 template <class Cfg>
 sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows, const void* q_w,
                          const float* s_w, const int32_t* offsets, void* y, int64_t T, int64_t M,
@@ -818,30 +847,23 @@ sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows,
       if (!make_map(&tx.m[i], q_a, false, k, static_cast<uint64_t>(M), 128, 16u << i))
         return SQ_ERR_CUDA;
   }
-  static std::atomic<int> max_clusters[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SQ_ERR_CUDA;
+  // most tiles the offsets can give: each group of rows ends in at most one partial tile
+  const int64_t tiles_n = (N + 255) / 256;
+  const int64_t tiles = ((T < E ? T : E) + T / Cfg::BT) * tiles_n;
   const int smem = Cfg::smem_bytes();
-  int mc = max_clusters[dev].load(std::memory_order_acquire);
-  if (mc <= 0) {
-    if (cudaFuncSetAttribute(grouped_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess)
-      return SQ_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(Cfg::THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&mc, grouped_kernel<Cfg>, &cfg) != cudaSuccess || mc <= 0)
-      return SQ_ERR_CUDA;
-    max_clusters[dev].store(mc, std::memory_order_release);
+  // A tile's K over 4 or 2 pairs where every tile can have a resident cluster of its own
+  // and a pair keeps two K blocks or more.  (2 rows, K = N = 2048: see grouped.cuh.)
+  int split = 1, mc = 0;
+  if constexpr (Cfg::SPLIT) {
+    for (split = 4; split > 1; split /= 2) {
+      if (K / 128 < 2 * split) continue;
+      mc = grouped_clusters<Cfg>(split, smem);
+      if (mc <= 0) return SQ_ERR_CUDA;
+      if (tiles <= mc) break;
+    }
   }
+  if (split == 1) mc = grouped_clusters<Cfg>(1, smem);
+  if (mc <= 0) return SQ_ERR_CUDA;
   GroupedArgs g{};
   g.offsets = offsets;
   g.rows = rows;
@@ -853,12 +875,11 @@ sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows,
   g.E = static_cast<int>(E);
   g.N = static_cast<int>(N);
   g.kb_total = static_cast<int>(K / 128);
-  g.tiles_n = static_cast<int>((N + 255) / 256);
-  // most tiles the offsets can give: each group of rows ends in at most one partial tile
-  const int64_t tiles = ((T < E ? T : E) + T / Cfg::BT) * g.tiles_n;
+  g.tiles_n = static_cast<int>(tiles_n);
+  g.split = split;
   const int clusters = tiles < mc ? static_cast<int>(tiles) : mc;
-  return launch_dependent(grouped_kernel<Cfg>, static_cast<unsigned>(2 * clusters), Cfg::THREADS,
-                          smem, st, 2, tw, tx, g);
+  return launch_dependent(grouped_kernel<Cfg>, static_cast<unsigned>(2 * split * clusters),
+                          Cfg::THREADS, smem, st, 2 * split, tw, tx, g);
 }
 
 sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* rows,
