@@ -39,6 +39,7 @@ def test_grouped_checks(lib, name):
     assert call(T=1 << 31) == 2 and call(M=1 << 31) == 2
     assert call(E=1024, N=1 << 22) == 2                          # E N past 32 bits
     assert call(T=(1 << 31) - 1000, N=1 << 20) == 2              # tiles past 32 bits
+    assert call(T=1 << 30, M=1 << 30, N=65536) == 2              # with 128-row tiles
     assert call((None,) * 7, T=0, M=0) == 0                      # nothing to do
     assert f(*(OK,) * 7, 4, 4, 2, 144, 256, None) == 2 if name.startswith("fp8") else True
 

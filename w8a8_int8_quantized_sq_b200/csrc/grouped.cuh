@@ -6,9 +6,11 @@
 // offsets[e+1] - 1 and multiplies them by its own weights q_w[e] (N x K).  Row t
 // reads token rows[t] (or token t when rows is NULL).  The offsets live on the
 // device, so every CTA works the tile list out for itself: expert e has
-// ceil(r_e / 256) token tiles of nearly equal size times ceil(N / 256) channel
+// ceil(r_e / BT) token tiles of nearly equal size times ceil(N / 256) channel
 // tiles; clusters take tiles round-robin, token tiles of one weight tile
-// next to each other so that the weights come from L2 after the first.
+// next to each other so that the weights come from L2 after the first.  (Giving each
+// cluster a contiguous range of equal cost instead made a 32768-row prefill 35 %
+// slower: the ranges' weight tiles no longer meet in L2.)
 //
 // Operand roles: the weights fill the 256 MMA rows (128 channels in each CTA's
 // tensor memory) and the tokens are the MMA's N, which is an operand of the
@@ -21,14 +23,31 @@
 // FP8: every 128-wide K block is a fresh accumulator and is promoted into fp32
 // registers, acc = fmaf(P_kb, f32(s_a * s_w), acc).  A CTA's 128 channels are
 // one weight block, so s_w is uniform and the products s_a * s_w of a K block are
-// one vector over the tile's tokens: a scale warp writes it to a shared-memory
-// ring one K block ahead.  Its arrival counts on the barrier on which the K
-// block's MMAs report, so the epilogue waits once for both.
+// one vector over the tile's tokens, which scale warps write to a shared-memory ring.
 //
-// Roles per CTA: warp 0 TMA producer, warp 1 tensor-memory allocation (pair)
-// and, in the leader CTA, the MMA issuer, warp 2 scales (FP8 only), the others
-// epilogue.  Token rows are fetched by tile loads when rows is NULL and by
-// four-row gather loads otherwise.  No load uses multicast.
+// Roles per CTA: warp 0 loads weights and, when rows is NULL, tokens (TMA tiles);
+// warp 1 allocates the tensor memory (pair), issues the MMAs in the leader CTA and in
+// the other relays the epilogue's releases; then the scale warps, the warps that issue
+// four-row gather loads when rows is given, and the epilogue.  The epilogue reads the
+// accumulators as matrix fragments (a lane sees a quarter of the tokens, hence few scale
+// reads) and stores through a transposing matrix store.  No load uses multicast.
+//
+// What bounds it, measured on one B200 (INT8 codes of normal values unless said):
+//   INT8, 8 experts x 1024 rows, N = 8192: K = 5120 225-232 us (3000 TOPS; 4030 with zero
+//     codes, so the power limit, not the pipeline), K = 2048 98-102 us (2750 TOPS).
+//   INT8, 32768 rows over 64 experts, K = N = 2048: 123-127 us (132-137 us gathered; 104 us
+//     with zero codes).  Token tiles that are not full and the uneven last wave cost the rest.
+//   INT8, 128 rows over 64 experts, K = 2048, N = 1536: 36 us, 5.5 TB/s of weights.
+//   FP8, 8198 rows over 8 experts, K = 5120, N = 2048: 138 us, 1240 TOPS (148 us
+//     gathered).  The epilogue's own chain per K block (tensor-memory reads of 64 bytes
+//     per clock and SM quadrant, releases, fused multiply-adds) takes 780 cycles; with
+//     the promotion left out the call takes 115 us, the loads and MMAs alone 87 us.
+//     Slower variants: lanes as channels with broadcast scales (220 us), 16 epilogue
+//     warps of 32 columns (143 us but decode 6 % slower), 192- and 256-token tiles with two
+//     accumulators (240-400 us), waits with the suspend hint (240 us).
+//   FP8, 222 rows over 64 experts, K = 1408, N = 2048: 37 us, 5.0 TB/s of weights.
+//   Token rows copied by cp.async threads instead of TMA ran 2-3 times slower (the
+//   proxy fences wait for every copy in flight).
 #pragma once
 #include "gemm3.cuh"
 
@@ -103,10 +122,10 @@ struct GroupedCfg {
   static_assert(!F8 || BT <= 128, "FP8 epilogue: two groups of at most 64 columns");
 };
 
-// mbarrier wait of the MMA issuer and its relay, bounded like wait_bounded, the same
-// answer in every lane.  No suspend-time hint: the accumulators' round trip (MMA,
-// commit, epilogue, release, MMA) took 8 % longer with the hint of the other waits.
-// The other roles keep it, since their polling takes issue slots from the epilogue.
+// mbarrier wait without a suspend-time hint, bounded like wait_bounded, the same answer
+// in every lane: for the accumulators' round trip (MMA, commit, epilogue, release,
+// MMA), where waking from the hint's suspension showed (FP8 prefill 243 us against
+// 203 us).  The other roles keep the hint: their polling would take issue slots.
 __device__ __forceinline__ bool prompt_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -336,9 +355,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tmem_relinquish_pair();
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tmW);
-  griddep_wait();  // nothing above touches global memory: the launch may overlap any kernel
+  // Nothing above touches global memory, so the launch may overlap any kernel.  What that
+  // kernel may have written is read below through L2, not through the read-only path.
+  griddep_wait();
   // offsets, held inside [0, T] and non-decreasing whatever the caller wrote
-  for (int e = threadIdx.x; e <= g.E; e += Cfg::THREADS) lo[e] = min(max(__ldg(g.offsets + e), 0), g.T);
+  for (int e = threadIdx.x; e <= g.E; e += Cfg::THREADS) lo[e] = min(max(__ldcg(g.offsets + e), 0), g.T);
   __syncthreads();
   if (warp == 0) {
     int top = 0, tiles = 0;
@@ -382,230 +403,230 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   griddep_launch_dependents();
 
   if (warp < Cfg::EPI0) {
-   if constexpr (Cfg::F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::CONTROL_REGS));
-   if (warp == 0) {
-    // ------------------------------- weights, and tokens in row order (TMA)
-    if (lane == 0) {
-      const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
-      const uint64_t pol = policy_evict_normal();
-      GroupedWalk walk(lo, cum, g.tiles_n);
-      uint32_t stage = 0, phase = 0;
-      long long fills = 0;
-      bool ok = true;
-      for (int t = cluster; ok && t < num_tiles; t += nclusters) {
-        const GroupedTile tile = walk.at(t);
-        const int half = ((tile.nrows + 31) & ~31) >> 1;  // token rows staged by this CTA
-        const int w_row = tile.e * g.N + tile.ct * 256 + static_cast<int>(rank) * 128;
-        const int x_row = tile.row0 + static_cast<int>(rank) * half;
-        // the smallest box of 16 << box rows that holds the half
-        const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-        const uint32_t bytes = 2 * (Cfg::A_BYTES + (g.rows ? half : 16 << box) * 128);
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (leader) mbar_arrive_expect_tx(full + stage, bytes);
-          tma_load_2d_pair(smA + stage * Cfg::A_BYTES, &tmW, (k0 + kb) * 128, w_row,
-                           full_leader + stage * 8, pol);
-          if (!g.rows)
-            tma_load_2d_pair(smB + stage * Cfg::B_BYTES, &tmX.m[box], (k0 + kb) * 128, x_row,
+    if constexpr (Cfg::F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::CONTROL_REGS));
+    if (warp == 0) {
+      // ------------------------------- weights, and tokens in row order (TMA)
+      if (lane == 0) {
+        const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
+        const uint64_t pol = policy_evict_normal();
+        GroupedWalk walk(lo, cum, g.tiles_n);
+        uint32_t stage = 0, phase = 0;
+        long long fills = 0;
+        bool ok = true;
+        for (int t = cluster; ok && t < num_tiles; t += nclusters) {
+          const GroupedTile tile = walk.at(t);
+          const int half = ((tile.nrows + 31) & ~31) >> 1;  // token rows staged by this CTA
+          const int w_row = tile.e * g.N + tile.ct * 256 + static_cast<int>(rank) * 128;
+          const int x_row = tile.row0 + static_cast<int>(rank) * half;
+          // the smallest box of 16 << box rows that holds the half
+          const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+          const uint32_t bytes = 2 * (Cfg::A_BYTES + (g.rows ? half : 16 << box) * 128);
+          for (int kb = 0; kb < nk; ++kb) {
+            if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (leader) mbar_arrive_expect_tx(full + stage, bytes);
+            tma_load_2d_pair(smA + stage * Cfg::A_BYTES, &tmW, (k0 + kb) * 128, w_row,
                              full_leader + stage * 8, pol);
-          ++fills;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            if (!g.rows)
+              tma_load_2d_pair(smB + stage * Cfg::B_BYTES, &tmX.m[box], (k0 + kb) * 128, x_row,
+                               full_leader + stage * 8, pol);
+            ++fills;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
+        if (leader) {
+          // the pair's copies (both CTAs' bytes count here) have all landed
+          for (int st = 0; st < STAGES; ++st) {
+            const long long n = fills / STAGES + (st < fills % STAGES ? 1 : 0);
+            if (n > 0) wait_drain(full + st, static_cast<uint32_t>((n - 1) & 1));
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------ MMA issuer (leader), relay (other CTA)
+      // The other CTA's releases of an accumulator reach the leader as one arrival: its
+      // epilogue warps arrive on their own CTA's barrier and this warp passes it on.
+      if (!leader) {
+        const uint32_t tfree_leader = mapa_shared(smem_u32(tfree), lead);
+        uint32_t local = 0;
+        bool ok = true;
+        for (int t = cluster; ok && t < num_tiles; t += nclusters)
+          for (int i = 0; i < (Cfg::F8 ? nk : 1); ++i, ++local) {
+            const uint32_t a = local % NACC, u = local / NACC;
+            if (!prompt_wait(tfree + a, u & 1u, abort_flag)) { ok = false; break; }
+            if (lane == 0) mbar_arrive_remote(tfree_leader + a * 8);
+            __syncwarp();
+          }
       }
       if (leader) {
-        // the pair's copies (both CTAs' bytes count here) have all landed
-        for (int st = 0; st < STAGES; ++st) {
-          const long long n = fills / STAGES + (st < fills % STAGES ? 1 : 0);
-          if (n > 0) wait_drain(full + st, static_cast<uint32_t>((n - 1) & 1));
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------ MMA issuer (leader), relay (other CTA)
-    // The other CTA's releases of an accumulator reach the leader as one arrival: its
-    // epilogue warps arrive on their own CTA's barrier and this warp passes it on.
-    if (!leader) {
-      const uint32_t tfree_leader = mapa_shared(smem_u32(tfree), lead);
-      uint32_t local = 0;
-      bool ok = true;
-      for (int t = cluster; ok && t < num_tiles; t += nclusters)
-        for (int i = 0; i < (Cfg::F8 ? nk : 1); ++i, ++local) {
-          const uint32_t a = local % NACC, u = local / NACC;
-          if (!prompt_wait(tfree + a, u & 1u, abort_flag)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_remote(tfree_leader + a * 8);
-          __syncwarp();
-        }
-    }
-    if (leader) {
-      GroupedWalk walk(lo, cum, g.tiles_n);
-      uint32_t stage = 0, phase = 0, local = 0;
-      bool ok = true;
-      for (int t = cluster; ok && t < num_tiles; t += nclusters) {
-        const GroupedTile tile = walk.at(t);
-        const int n = (tile.nrows + 31) & ~31;
-        const uint32_t idesc = Cfg::F8 ? idesc_e4m3_f32_m256(n) : idesc_i8_s32_m256(n);
-        uint32_t d = 0;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (Cfg::F8 || kb == 0) {  // a free accumulator: per K block (FP8) or per tile
-            const uint32_t a = local % NACC, u = local / NACC;
-            ++local;
-            ok = prompt_wait2(tfree + a, (u & 1u) ^ 1u, full + stage, phase, abort_flag);
-            d = tmem + a * BT;
-          } else {
-            ok = prompt_wait(full + stage, phase, abort_flag);
-          }
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smA + stage * Cfg::A_BYTES);
-          const uint32_t sb = smem_u32(smB + stage * Cfg::B_BYTES);
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t acc = (k > 0 || (!Cfg::F8 && kb > 0)) ? 1u : 0u;
-              if constexpr (Cfg::F8)
-                mma_f8_pair(d, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32), idesc, acc);
-              else
-                mma_i8_pair(d, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32), idesc, acc);
+        GroupedWalk walk(lo, cum, g.tiles_n);
+        uint32_t stage = 0, phase = 0, local = 0;
+        bool ok = true;
+        for (int t = cluster; ok && t < num_tiles; t += nclusters) {
+          const GroupedTile tile = walk.at(t);
+          const int n = (tile.nrows + 31) & ~31;
+          const uint32_t idesc = Cfg::F8 ? idesc_e4m3_f32_m256(n) : idesc_i8_s32_m256(n);
+          uint32_t d = 0;
+          for (int kb = 0; kb < nk; ++kb) {
+            if (Cfg::F8 || kb == 0) {  // a free accumulator: per K block (FP8) or per tile
+              const uint32_t a = local % NACC, u = local / NACC;
+              ++local;
+              ok = prompt_wait2(tfree + a, (u & 1u) ^ 1u, full + stage, phase, abort_flag);
+              d = tmem + a * BT;
+            } else {
+              ok = prompt_wait(full + stage, phase, abort_flag);
             }
-            commit_pair(empty + stage, lead);
-            if (Cfg::F8 || kb == nk - 1) commit_pair(tfull + (local - 1) % NACC, lead);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smA + stage * Cfg::A_BYTES);
+            const uint32_t sb = smem_u32(smB + stage * Cfg::B_BYTES);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t acc = (k > 0 || (!Cfg::F8 && kb > 0)) ? 1u : 0u;
+                if constexpr (Cfg::F8)
+                  mma_f8_pair(d, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32), idesc, acc);
+                else
+                  mma_i8_pair(d, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32), idesc, acc);
+              }
+              commit_pair(empty + stage, lead);
+              if (Cfg::F8 || kb == nk - 1) commit_pair(tfull + (local - 1) % NACC, lead);
+            }
+            __syncwarp();
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          __syncwarp();
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (elect_one()) {
+          mma_commit_pair(drain);
+          wait_drain(drain, 0);
         }
       }
-      if (elect_one()) {
-        mma_commit_pair(drain);
-        wait_drain(drain, 0);
+      __syncwarp();
+    } else if (warp >= 2 + Cfg::NS) {
+      // ---------------------------------------------------- gathered tokens
+      // Each lane fetches four rows of a stage; lane l of warp w takes rows 4 (NG l +
+      // w) and up, so that the warps share the loads evenly.  A load takes its warp
+      // about 80 cycles to issue: from one warp alone they made the prefill of
+      // 32768 rows over 64 experts, K = N = 2048, take 346 us, from four 152 us,
+      // from eight 140 us.
+      if (g.rows) {
+        const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
+        const int j = (lane * Cfg::NG + warp - 2 - Cfg::NS) * 4;
+        GroupedWalk walk(lo, cum, g.tiles_n);
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int t = cluster; ok && t < num_tiles; t += nclusters) {
+          const GroupedTile tile = walk.at(t);
+          const int half = ((tile.nrows + 31) & ~31) >> 1;
+          const int first = static_cast<int>(rank) * half + j;
+          // rows past the tile or outside the tokens are fetched as zeros
+          auto token = [&](int i) {
+            if (first + i >= tile.nrows) return g.M;
+            const int r = __ldcg(g.rows + tile.row0 + first + i);
+            return static_cast<unsigned>(r) < static_cast<unsigned>(g.M) ? r : g.M;
+          };
+          const bool mine = j < half;
+          int4 r4 = make_int4(g.M, g.M, g.M, g.M);
+          if (mine) r4 = make_int4(token(0), token(1), token(2), token(3));
+          for (int kb = 0; kb < nk; ++kb) {
+            if (!warp_wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (mine)
+              tma_gather4_pair(smB + stage * Cfg::B_BYTES + j * 128, &tmX.m[0], (k0 + kb) * 128, r4,
+                               full_leader + stage * 8);
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
       }
-    }
-    __syncwarp();
-  } else if (warp >= 2 + Cfg::NS) {
-    // ---------------------------------------------------- gathered tokens
-    // Each lane fetches four rows of a stage; lane l of warp w takes rows 4 (NG l +
-    // w) and up, so that the warps share the loads evenly.  A load takes its warp
-    // about 80 cycles to issue: from one warp alone they made the prefill of
-    // 32768 rows over 64 experts, K = N = 2048, take 346 us, from four 152 us,
-    // from eight 140 us.
-    if (g.rows) {
-      const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
-      const int j = (lane * Cfg::NG + warp - 2 - Cfg::NS) * 4;
+    } else {
+      // ------------------------------------------------------------- scales
+      // A ring slot holds SV vectors over the tile's tokens: INT8 the tile's s_tok; FP8 s_a *
+      // s_w of four K blocks (0 for rows outside).  FP8: two warps fill slots in turn,
+      // each with its next slot's loads in flight.  One warp that loaded, wrote and
+      // then loaded again gave four K blocks per L2 latency, and decode of 222
+      // rows over 64 experts (K = 1408, N = 2048) took 55 us.
+      constexpr int NV = BT / 32;
       GroupedWalk walk(lo, cum, g.tiles_n);
-      uint32_t stage = 0, phase = 0;
+      uint32_t slot = 0, phase = 0;
+      const uint32_t mine = warp - 2;  // FP8: the slots of this parity
       bool ok = true;
       for (int t = cluster; ok && t < num_tiles; t += nclusters) {
         const GroupedTile tile = walk.at(t);
-        const int half = ((tile.nrows + 31) & ~31) >> 1;
-        const int first = static_cast<int>(rank) * half + j;
-        // rows past the tile or outside the tokens are fetched as zeros
-        auto token = [&](int i) {
-          if (first + i >= tile.nrows) return g.M;
-          const int r = __ldg(g.rows + tile.row0 + first + i);
-          return static_cast<unsigned>(r) < static_cast<unsigned>(g.M) ? r : g.M;
-        };
-        const bool mine = j < half;
-        int4 r4 = make_int4(g.M, g.M, g.M, g.M);
-        if (mine) r4 = make_int4(token(0), token(1), token(2), token(3));
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!warp_wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (mine)
-            tma_gather4_pair(smB + stage * Cfg::B_BYTES + j * 128, &tmX.m[0], (k0 + kb) * 128, r4,
-                             full_leader + stage * 8);
-          __syncwarp();
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        int tok[NV];  // token of column 32 i + lane, -1: none
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = i * 32 + lane;
+          tok[i] = -1;
+          if (c < tile.nrows) {
+            const int r = g.rows ? __ldcg(g.rows + tile.row0 + c) : tile.row0 + c;
+            if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M)) tok[i] = r;
           }
         }
-      }
-    }
-  } else {
-    // ------------------------------------------------------------- scales
-    // A ring slot holds SV vectors over the tile's tokens: INT8 the tile's s_tok; FP8 s_a *
-    // s_w of four K blocks (0 for rows outside).  FP8: two warps fill slots in turn,
-    // each with its next slot's loads in flight.  One warp that loaded, wrote and
-    // then loaded again gave four K blocks per L2 latency, and decode of 222
-    // rows over 64 experts (K = 1408, N = 2048) took 55 us.
-    constexpr int NV = BT / 32;
-    GroupedWalk walk(lo, cum, g.tiles_n);
-    uint32_t slot = 0, phase = 0;
-    const uint32_t mine = warp - 2;  // FP8: the slots of this parity
-    bool ok = true;
-    for (int t = cluster; ok && t < num_tiles; t += nclusters) {
-      const GroupedTile tile = walk.at(t);
-      int tok[NV];  // token of column 32 i + lane, -1: none
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = i * 32 + lane;
-        tok[i] = -1;
-        if (c < tile.nrows) {
-          const int r = g.rows ? __ldg(g.rows + tile.row0 + c) : tile.row0 + c;
-          if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M)) tok[i] = r;
-        }
-      }
-      auto next_slot = [&]() {
-        if (++slot == Cfg::SSLOTS) { slot = 0; phase ^= 1u; }
-      };
-      if constexpr (!Cfg::F8) {
-        float v[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = tok[i] >= 0 ? __ldg(g.s_a + tok[i]) : 0.0f;
-        if (!warp_wait_bounded(sfree + slot, phase ^ 1u, abort_flag)) { ok = false; break; }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) ring[slot * BT + i * 32 + lane] = v[i];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfull + slot);
-        next_slot();
-      } else {
-        const int ch0 = tile.ct * 256 + static_cast<int>(rank) * 128;
-        const float* sw = g.s_w + (static_cast<size_t>(tile.e) * (g.N >> 7) + (ch0 < g.N ? ch0 >> 7 : 0)) * kbt + k0;
-        const bool wide = ((kbt | k0) & 3) == 0;  // a token's scales can be loaded four K blocks at a time
-        // scales of K blocks kb .. kb + 3 (0 past the last)
-        auto load4 = [&](const float* p, int kb) {
-          if (wide) return __ldg(reinterpret_cast<const float4*>(p + kb));
-          return make_float4(__ldg(p + kb), kb + 1 < nk ? __ldg(p + kb + 1) : 0.0f,
-                             kb + 2 < nk ? __ldg(p + kb + 2) : 0.0f,
-                             kb + 3 < nk ? __ldg(p + kb + 3) : 0.0f);
+        auto next_slot = [&]() {
+          if (++slot == Cfg::SSLOTS) { slot = 0; phase ^= 1u; }
         };
-        float4 w, v[NV];
-        auto fetch = [&](int kb) {
-          w = load4(sw, kb);
+        if constexpr (!Cfg::F8) {
+          float v[NV];
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
-            v[i] = tok[i] >= 0 ? load4(g.s_a + static_cast<size_t>(tok[i]) * kbt + k0, kb)
-                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        };
-        int kb = (slot & 1u) == mine ? 0 : 4;  // this warp's first batch of the tile
-        if (kb < nk) fetch(kb);
-        for (int b = 0; b < nk; b += 4, next_slot()) {
-          if ((slot & 1u) != mine) continue;
+          for (int i = 0; i < NV; ++i) v[i] = tok[i] >= 0 ? __ldcg(g.s_a + tok[i]) : 0.0f;
           if (!warp_wait_bounded(sfree + slot, phase ^ 1u, abort_flag)) { ok = false; break; }
-          float* to = ring + slot * (Cfg::SV * BT) + lane;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            to[i * 32] = __fmul_rn(v[i].x, w.x);
-            to[BT + i * 32] = __fmul_rn(v[i].y, w.y);
-            to[2 * BT + i * 32] = __fmul_rn(v[i].z, w.z);
-            to[3 * BT + i * 32] = __fmul_rn(v[i].w, w.w);
-          }
+          for (int i = 0; i < NV; ++i) ring[slot * BT + i * 32 + lane] = v[i];
           __syncwarp();
           if (lane == 0) mbar_arrive(sfull + slot);
-          kb += 8;
+          next_slot();
+        } else {
+          const int ch0 = tile.ct * 256 + static_cast<int>(rank) * 128;
+          const float* sw = g.s_w + (static_cast<size_t>(tile.e) * (g.N >> 7) + (ch0 < g.N ? ch0 >> 7 : 0)) * kbt + k0;
+          const bool wide = ((kbt | k0) & 3) == 0;  // a token's scales can be loaded four K blocks at a time
+          // scales of K blocks kb .. kb + 3 (0 past the last)
+          auto load4 = [&](const float* p, int kb) {
+            if (wide) return __ldcg(reinterpret_cast<const float4*>(p + kb));
+            return make_float4(__ldcg(p + kb), kb + 1 < nk ? __ldcg(p + kb + 1) : 0.0f,
+                               kb + 2 < nk ? __ldcg(p + kb + 2) : 0.0f,
+                               kb + 3 < nk ? __ldcg(p + kb + 3) : 0.0f);
+          };
+          float4 w, v[NV];
+          auto fetch = [&](int kb) {
+            w = load4(sw, kb);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+              v[i] = tok[i] >= 0 ? load4(g.s_a + static_cast<size_t>(tok[i]) * kbt + k0, kb)
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          };
+          int kb = (slot & 1u) == mine ? 0 : 4;  // this warp's first batch of the tile
           if (kb < nk) fetch(kb);
+          for (int b = 0; b < nk; b += 4, next_slot()) {
+            if ((slot & 1u) != mine) continue;
+            if (!warp_wait_bounded(sfree + slot, phase ^ 1u, abort_flag)) { ok = false; break; }
+            float* to = ring + slot * (Cfg::SV * BT) + lane;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+              to[i * 32] = __fmul_rn(v[i].x, w.x);
+              to[BT + i * 32] = __fmul_rn(v[i].y, w.y);
+              to[2 * BT + i * 32] = __fmul_rn(v[i].z, w.z);
+              to[3 * BT + i * 32] = __fmul_rn(v[i].w, w.w);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sfull + slot);
+            kb += 8;
+            if (kb < nk) fetch(kb);
+          }
         }
       }
     }
-   }
   } else {
     if constexpr (Cfg::F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::EPI_REGS));
     // ------------------------------------------------------------ epilogue
@@ -661,7 +682,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = ch + 8 * k + (lane >> 2);
-          s_ch[k] = c < g.N ? __ldg(g.s_w + static_cast<size_t>(tile.e) * N + c) : 0.0f;
+          s_ch[k] = c < g.N ? __ldcg(g.s_w + static_cast<size_t>(tile.e) * N + c) : 0.0f;
         }
         const uint32_t a = local % NACC, u = local / NACC;
         const uint32_t r = local % Cfg::SSLOTS, ur = local / Cfg::SSLOTS;
@@ -711,7 +732,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         uint64_t acc[2][2][8];  // pairs of fp32 sums of neighbouring tokens
 #pragma unroll
         for (int j = 0; j < 32; ++j) (&acc[0][0][0])[j] = 0;
-        uint32_t v[2][2][16];  // one chunk loads while the other is added
+        uint32_t v[2][2][16];   // one K block's partials
+        uint64_t f[2][4] = {};  // and scales (pairs)
         const uint32_t src = lanes + col0;
         // acc += partials * scales of one chunk
         auto add = [&](uint64_t (&x)[2][8], const uint32_t (&y)[2][16], const uint64_t (&f)[4]) {
@@ -723,55 +745,48 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               for (int r = 2 * i; r < 2 * i + 2; ++r)
                 x[h][r] = fma2(y[h][2 * r], y[h][2 * r + 1], f[i], x[h][r]);
         };
-        // A poll, a scale read and a tensor-memory read each take over 100 cycles even when
-        // everything is ready, so K blocks are taken in pairs on one poll (commits arrive in
-        // order: the second is complete after the first), and each read is issued
-        // before the arithmetic that does not need it: the second chunk's load before the
-        // first is added, the next block's first before the second is added.
-        auto load_scales = [&](uint64_t (&f)[4], int kb, int c) {
-          const float* s = ring + (sslot * Cfg::SV + (kb & 3)) * BT + col0 + c + (lane & 3) * 2;
+        // K blocks are taken in pairs on one poll (a poll takes over 100 cycles even when it
+        // succeeds; commits arrive in order, so the second is complete after the
+        // first), and a block's partials are requested as soon as the registers are free.
+        auto load_scales = [&](int kb) {
+          const float* s = ring + (sslot * Cfg::SV + (kb & 3)) * BT + (has0 ? col0 : 0) + (lane & 3) * 2;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const uint64_t*>(s + i * 8);
+          for (int i = 0; i < 4; ++i) {
+            f[0][i] = *reinterpret_cast<const uint64_t*>(s + i * 8);
+            if constexpr (BT > 32) f[1][i] = *reinterpret_cast<const uint64_t*>(s + 32 + i * 8);
+          }
+        };
+        auto load_block = [&](uint32_t l) {
+          if (has0) tmem_frags_async(src + l % NACC * BT, v[0]);
+          if (has1) tmem_frags_async(src + l % NACC * BT + 32, v[1]);
+        };
+        auto add_block = [&](uint32_t l) {
+          tmem_frags_wait(v[0]);
+          tmem_frags_wait(v[1]);
+          release(l % NACC);  // the K block is in registers
+          if (has0) add(acc[0], v[0], f[0]);
+          if (has1) add(acc[1], v[1], f[1]);
         };
         const uint32_t l1 = local + (nk > 1 ? 1 : 0);
         if (!prompt_wait(tfull + l1 % NACC, l1 / NACC & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        if (has0) tmem_frags_async(src + local % NACC * BT, v[0]);
-        if (has1) tmem_frags_async(src + local % NACC * BT + 32, v[1]);
-        uint64_t f[2][4] = {};
-        // One K block whose first chunk is in flight; `load_next` may request the next
-        // block's first chunk (into v[0]) once this one's is used.
-        auto block = [&](uint32_t a, int kb, auto&& load_next) {
-          tmem_frags_wait(v[0]);
-          tmem_frags_wait(v[1]);
-          release(a);
-          if (has0) add(acc[0], v[0], f[0]);
-          if (has1) add(acc[1], v[1], f[1]);
-          load_next();
-        };
+        load_block(local);
         for (int kb = 0; kb < nk; kb += 2) {
           if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) { ok = false; break; }
-          load_scales(f[0], kb, 0);
-          if constexpr (BT > 32) load_scales(f[1], kb, 32);
+          load_scales(kb);
           const bool two = kb + 1 < nk, more = kb + 2 < nk;
-          const uint32_t a = local % NACC, a1 = (local + 1) % NACC;
           const uint32_t l2 = local + 2, l3 = kb + 3 < nk ? local + 3 : l2;  // the next pair
           const bool polled = more && prompt_try_wait(smem_u32(tfull + l3 % NACC), l3 / NACC & 1u);
-          bool early = false;
-          auto next_pair = [&]() {
-            early = __all_sync(0xffffffffu, polled);
-            if (early) {
-              tc_fence_after();
-              { if (has0) tmem_frags_async(src + l2 % NACC * BT, v[0]); if (has1) tmem_frags_async(src + l2 % NACC * BT + 32, v[1]); }
-            }
-          };
+          add_block(local);
           if (two) {
-            block(a, kb, [&]() { { if (has0) tmem_frags_async(src + a1 * BT, v[0]); if (has1) tmem_frags_async(src + a1 * BT + 32, v[1]); } });
-            load_scales(f[0], kb + 1, 0);
-            if constexpr (BT > 32) load_scales(f[1], kb + 1, 32);
-            block(a1, kb + 1, next_pair);
-          } else {
-            block(a, kb, next_pair);
+            load_block(local + 1);
+            load_scales(kb + 1);
+            add_block(local + 1);
+          }
+          const bool early = __all_sync(0xffffffffu, polled);
+          if (early) {
+            tc_fence_after();
+            load_block(l2);
           }
           if ((kb & 2) || !more) {  // done with the slot's vectors
             __syncwarp();
@@ -782,7 +797,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (more && !early) {
             if (!prompt_wait(tfull + l3 % NACC, l3 / NACC & 1u, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            { if (has0) tmem_frags_async(src + l2 % NACC * BT, v[0]); if (has1) tmem_frags_async(src + l2 % NACC * BT + 32, v[1]); }
+            load_block(l2);
           }
         }
         if (!ok) break;
@@ -818,6 +833,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
       }
     }
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");  // a wait may have given up before it
   }
 
   tc_fence_before();

@@ -81,12 +81,14 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
       const int c = (j * TPR + t) * 8;
       x[j] = y[j] = make_uint4(0, 0, 0, 0);
       if (row < p.M && c < K) {
-        if constexpr (OP == RQ_ADD_NORM) {  // plain loads: b_out may be one of the inputs
+        // plain loads: b_out may be one of the inputs, and a kernel that this launch
+        // overlaps may have written any of them
+        if constexpr (OP == RQ_ADD_NORM) {
           x[j] = *reinterpret_cast<const uint4*>(p.a + row * K + c);
           y[j] = *reinterpret_cast<const uint4*>(p.b + row * K + c);
         } else {
-          x[j] = __ldg(reinterpret_cast<const uint4*>(p.a + row * 2 * K + c));
-          y[j] = __ldg(reinterpret_cast<const uint4*>(p.a + row * 2 * K + K + c));
+          x[j] = *reinterpret_cast<const uint4*>(p.a + row * 2 * K + c);
+          y[j] = *reinterpret_cast<const uint4*>(p.a + row * 2 * K + K + c);
         }
       }
     }
@@ -139,8 +141,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
       for (int j = 0; j < NV; ++j) {
         const int c = (j * TPR + t) * 8;
         if (c < K) {
-          const float4 g0 = __ldg(reinterpret_cast<const float4*>(p.vec + c));
-          const float4 g1 = __ldg(reinterpret_cast<const float4*>(p.vec + c) + 1);
+          const float4 g0 = *reinterpret_cast<const float4*>(p.vec + c);
+          const float4 g1 = reinterpret_cast<const float4*>(p.vec + c)[1];
           const float gm[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[j][i] = __fmul_rn(__fmul_rn(v[j][i], rn), gm[i]);
@@ -160,8 +162,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] = silu_mul(v[j][i], u[j][i]);
         if (p.vec && c < K) {
-          const float4 g0 = __ldg(reinterpret_cast<const float4*>(p.vec + c));
-          const float4 g1 = __ldg(reinterpret_cast<const float4*>(p.vec + c) + 1);
+          const float4 g0 = *reinterpret_cast<const float4*>(p.vec + c);
+          const float4 g1 = reinterpret_cast<const float4*>(p.vec + c)[1];
           const float gm[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[j][i] = __fmul_rn(v[j][i], gm[i]);

@@ -892,7 +892,7 @@ sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* 
   const int64_t most = (1ll << 31) - 1;
   // coordinates and tile numbers are 32-bit
   if (E * N + 256 > most || T + 256 > most) return SQ_ERR_SHAPE;
-  if ((E + T / 256 + 1) * ((N + 255) / 256) > most) return SQ_ERR_SHAPE;
+  if ((E + T / 128 + 1) * ((N + 255) / 256) > most) return SQ_ERR_SHAPE;  // 128: the narrower tiles
   if (M < 0 || M + 256 > most || (!rows && M != T)) return SQ_ERR_SHAPE;
   if (T == 0) return SQ_OK;
   if (M == 0) return SQ_ERR_SHAPE;
