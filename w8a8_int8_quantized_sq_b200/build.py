@@ -67,7 +67,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-DNDEBUG", "-shared", "-fPIC",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *[a for i in includes for a in ("-isystem", i)], BINDING_SRC, "-o", BINDING + ".tmp",
-          "-L" + HERE, "-l:libsqint8.so", "-L" + lib_dir, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+          "-L" + HERE, "-l:libsqint8.so", "-L" + lib_dir, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
           "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "_binding.so", verbose)
     os.replace(BINDING + ".tmp", BINDING)
     return BINDING

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -58,8 +59,10 @@ int device_of(const char* fn, const char* name, const at::Tensor& t, int64_t dim
   return t.get_device();
 }
 
+// Straight from the caching allocator: at::empty's dispatch costs as much again.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, dev)));
+  return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)),
+                                std::nullopt);
 }
 
 PyObject* fail(const char* fn, sq_status rc) {
