@@ -354,7 +354,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tmem_alloc_pair(tmem_holder, Cfg::TMEM_COLS);
     tmem_relinquish_pair();
   }
-  if (warp == 0 && lane == 0) tma_prefetch_desc(&tmW);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX.m[0]);
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers of every CTA initialised, tensor memory allocated in both of a pair
+  tc_fence_after();
   // Nothing above touches global memory, so the launch may overlap any kernel.  What that
   // kernel may have written is read below through L2, not through the read-only path.
   griddep_wait();
@@ -390,10 +396,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       tiles = __shfl_sync(0xffffffffu, n, 31);
     }
   }
-  tc_fence_before();
   __syncthreads();
-  cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated in both
-  tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int num_tiles = cum[g.E] * g.tiles_n;
   const int kbt = g.kb_total;
