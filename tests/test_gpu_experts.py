@@ -542,6 +542,131 @@ def test_layer_run_in_a_graph_and_on_streams(fmt):
     sq.check_device_error()
 
 
+@pytest.mark.parametrize("fmt", ["i8", "fp8"])
+def test_layer_run_after_joins_and_copies(fmt):
+    """Eager and captured: the first call after a join of two streams, after a copy and after
+    a fill sees what they wrote (every launch may overlap its predecessor's tail)."""
+    a = layer_inputs(24, 8, 3, 512, 256, fmt, 113)
+    args = cuda(*a[:5], *a[5]["up"], *a[5]["down"])
+    want = run_layer(*args, fmt)
+    torch.cuda.synchronize()
+    live = [torch.zeros_like(t) for t in args]
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for i in (0, 3, 4, 5, 7):
+                live[i].copy_(args[i])
+        for i in (1, 2, 6, 8):
+            live[i].copy_(args[i])
+        main.wait_stream(side)
+        kept, y = run_layer(*live, fmt)
+        live[0].zero_()             # after the run has read it
+        live[0].add_(args[0])
+        again = run_layer(*live, fmt)
+        return kept, y, *again
+
+    for _ in range(3):
+        for t in live:
+            t.zero_()
+        got = run()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want * 2):
+            assert torch.equal(g, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        for t in live:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want * 2):
+            assert torch.equal(g, w)
+
+
+def test_two_graphs_replayed_at_once():
+    """Nothing is shared between captured calls: two graphs replay on two streams together."""
+    runs = []
+    for seed in (114, 115):
+        a = layer_inputs(3, 8, 2, 1024, 512, "i8", seed)
+        args = cuda(*a[:5], *a[5]["up"], *a[5]["down"])
+        want = run_layer(*args, "i8")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run_layer(*args, "i8")
+        runs.append((graph, got, want, args, torch.cuda.Stream()))
+    for _ in range(20):
+        for graph, _, _, _, stream in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _, _ in runs:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------ large and many
+
+def test_grouped_i8_thousand_experts():
+    g = gen(131)
+    counts = torch.randint(0, 4, (1024,), generator=g).tolist()
+    c = i8_case(counts, 16, 128, True, 132)
+    y = sq.w8a8_grouped_mm(*cuda(*c[:5]), rows=cuda(c[5])[0])
+    assert_bits(y, i8_reference(*c, torch.zeros(sum(counts), 16, dtype=torch.bfloat16)), "y")
+
+
+@pytest.mark.parametrize("kind", ["i8", "fp8"])
+def test_grouped_output_past_32_bits(kind):
+    """More than 2^31 outputs: every row against the product of its token and expert."""
+    T, N = 1_100_003, 2048
+    c = (i8_case if kind == "i8" else fp8_case)([2, 2], N, 128, False, 133)
+    mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+    q_a, s_a, q_w, s_w = cuda(*c[:4])
+    cut = 700_001
+    rows = torch.randint(0, 4, (T,), generator=gen(134), dtype=torch.int32).cuda()
+    y = mm(q_a, s_a, q_w, s_w, torch.tensor([0, cut, T], dtype=torch.int32, device="cuda"), rows=rows)
+    each = [mm(q_a, s_a, q_w, s_w, torch.tensor(o, dtype=torch.int32, device="cuda"))
+            for o in ([0, 4, 4], [0, 0, 4])]
+    for e, (lo, hi) in enumerate(((0, cut), (cut, T))):
+        for at in range(lo, hi, 1 << 18):
+            end = min(hi, at + (1 << 18))
+            assert torch.equal(y[at:end], each[e][rows[at:end].long()])
+
+
+def test_grouped_weights_past_32_bits():
+    """More than 2^31 bytes of weights: the last experts' rows."""
+    E, N, K = 64, 8192, 4352
+    g = torch.Generator(device="cuda").manual_seed(135)
+    q_w = torch.randint(-127, 128, (E, N, K), generator=g, dtype=torch.int8, device="cuda")
+    q_a = torch.randint(-127, 128, (40, K), generator=g, dtype=torch.int8, device="cuda")
+    s_a, s_w = torch.full((40,), 0.01, device="cuda"), torch.full((E, N), 1e-3, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[E - 1], off[E] = 7, 40
+    y = sq.w8a8_grouped_mm(q_a, s_a, q_w, s_w, off.cuda()).cpu()
+    ref = i8_reference(q_a.cpu(), s_a.cpu(), q_w[E - 2:].cpu(), s_w[E - 2:].cpu(),
+                       torch.tensor([0, 7, 40]), None, torch.zeros(40, N, dtype=torch.bfloat16))
+    assert_bits(y, ref, "y")
+
+
+@pytest.mark.parametrize("fmt", ["i8", "fp8"])
+def test_row_operators_past_32_bits(fmt):
+    """More than 2^31 elements: the last rows equal the same rows alone."""
+    M, K = 420_001, 5120
+    h = torch.randn(64, K, device="cuda").bfloat16().repeat(M // 64 + 1, 1)[:M].contiguous()
+    gamma = torch.rand(K, device="cuda") + 0.25
+    got = call_norm(h, h, gamma, fmt)
+    want = call_norm(h[-70:].contiguous(), h[-70:].contiguous(), gamma, fmt)
+    for a, b in zip(got, want):
+        assert torch.equal(a[-70:], b)
+    del got, want
+    q, sc = call_silu(h, None, fmt)
+    q2, sc2 = call_silu(h[-70:].contiguous(), None, fmt)
+    assert torch.equal(q[-70:], q2) and torch.equal(sc[-70:], sc2)
+
+
 def test_refusals_on_the_gpu():
     q_a, s_tok, q_w, s_ch, off, rows = cuda(*i8_case([3, 2], 64, 256, True, 121))
     with pytest.raises(ValueError):
