@@ -7,6 +7,9 @@ together."""
 from __future__ import annotations
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -178,6 +181,38 @@ def test_grouped_padding_rows_give_zero(kind):
         assert torch.isnan(y.cpu()[1]).all() and torch.isfinite(y.cpu()[2:]).all()
     assert (y.cpu()[pad] == 0).all()
     assert not (y.cpu()[~pad] == 0).any()
+
+
+@pytest.mark.parametrize("T", [20, 90])
+@pytest.mark.parametrize("kind", ["i8", "fp8"])
+def test_grouped_padding_rows_give_zero_beside_nonfinite_weights(kind, T):
+    """A padding row is zero even where its expert's scales are infinite or NaN (FP8: and its
+    codes NaN); a token that no row reads and an expert without rows reach nothing."""
+    g = gen(43)
+    rows = torch.randint(0, 8, (T,), generator=g, dtype=torch.int32)
+    rows[1::3] = 9
+    rows[2::5] = -1
+    off = torch.tensor([0, T // 2, T // 2, T], dtype=torch.int32)
+    pad = (rows < 0) | (rows >= 8)
+    make = i8_case if kind == "i8" else fp8_case
+    mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+    q_a, s_a, q_w, s_w, _, _ = make([8, 0, 0], 256, 512, False, 44)
+    # token 5 unread, expert 1 without rows
+    rows[rows == 5] = 4
+    want = mm(*cuda(q_a, s_a, q_w, s_w, off), rows=rows.cuda()).cpu()
+    s_a[5], s_w[1] = float("nan"), float("inf")
+    if kind == "fp8":
+        q_a[5], q_w[1] = 0x7F, 0xFF
+    assert torch.equal(mm(*cuda(q_a, s_a, q_w, s_w, off), rows=rows.cuda()).cpu(), want)
+    # expert 2: every scale infinite, or every code NaN
+    s_w[2] = float("inf")
+    y = mm(*cuda(q_a, s_a, q_w, s_w, off), rows=rows.cuda()).cpu()
+    assert torch.equal(y[:T // 2], want[:T // 2])
+    assert (y[pad] == 0).all() and not torch.isfinite(y[T // 2:][~pad[T // 2:]]).any()
+    if kind == "fp8":
+        s_w[2], q_w[2] = 1.0, 0x7F
+        y = mm(*cuda(q_a, s_a, q_w, s_w, off), rows=rows.cuda()).cpu()
+        assert (y[pad] == 0).all() and torch.isnan(y[T // 2:][~pad[T // 2:]]).all()
 
 
 # ------------------------------------------------------------------------ FP8
@@ -585,6 +620,29 @@ def test_layer_run_after_joins_and_copies(fmt):
         torch.cuda.synchronize()
         for g, w in zip(got, want * 2):
             assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("fmt", ["i8", "fp8"])
+def test_layer_run_captured_as_the_first_calls_of_a_process(fmt):
+    """Nothing has to be called before a capture."""
+    code = f"""
+import torch
+import tests.test_gpu_experts as t
+a = t.layer_inputs(3, 8, 2, 512, 256, {fmt!r}, 116)
+args = t.cuda(*a[:5], *a[5]["up"], *a[5]["down"])
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = t.run_layer(*args, {fmt!r})
+graph.replay()
+torch.cuda.synchronize()
+want = t.run_layer(*args, {fmt!r})
+assert all(torch.equal(x, y) for x, y in zip(got, want))
+t.sq.check_device_error()
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": os.pathsep.join(p for p in sys.path if p)})
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_graphs_replayed_at_once():

@@ -107,7 +107,8 @@ struct GroupedCfg {
   static constexpr int PITCH = 80;               // bytes per token in a warp's store staging
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SC = OFF_B + STAGES * B_BYTES;
-  static constexpr int OFF_ST = OFF_SC + SSLOTS * SV * BT * 4;
+  static constexpr int OFF_VALID = OFF_SC + SSLOTS * SV * BT * 4;  // a bit per token and slot
+  static constexpr int OFF_ST = OFF_VALID + SSLOTS * ((BT / 32 * 4 + 15) & ~15);
   static constexpr int OFF_PART = OFF_ST + NE * 16 * PITCH;
   static constexpr int OFF_LO = OFF_PART + (SPLIT ? 3 * PART_BYTES : 0);
   static constexpr int OFF_CUM = OFF_LO + (kMaxExperts + 1) * 4;
@@ -269,11 +270,13 @@ struct GroupedWalk {
 // of tokens 8 b .. 8 b + 7 and channels 8 k .. 8 k + 7 (its row is the channel, its two
 // values two tokens).  A transposing matrix store puts every token's 32 channels
 // side by side in the warp's staging rows, which leave in 16-byte pieces.
-// out: token 0, channel 0 of the block; the first ntok tokens are stored; ch_ok:
-// channels 8 (lane % 4) .. + 7 exist.
+// out: token 0, channel 0 of the block; the first ntok tokens are stored, as zeros
+// where their bit in `valid` is clear (a padding row is zero whatever the expert's
+// weights and scales hold); ch_ok: channels 8 (lane % 4) .. + 7 exist.
 template <int PITCH>
 __device__ __forceinline__ void grouped_store(uint32_t st, __nv_bfloat16* out, size_t N, int lane,
-                                              const uint32_t (&p)[2][4], int ntok, bool ch_ok) {
+                                              const uint32_t (&p)[2][4], int ntok, uint32_t valid,
+                                              bool ch_ok) {
   const uint32_t to = st + (lane & 7) * PITCH + (lane >> 3) * 16;
   __syncwarp();  // the previous block has been read
 #pragma unroll
@@ -291,6 +294,7 @@ __device__ __forceinline__ void grouped_store(uint32_t st, __nv_bfloat16* out, s
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(st + t * PITCH + (lane & 3) * 16)
                  : "memory");
+    if (!(valid >> t & 1u)) v = make_uint4(0, 0, 0, 0);
     if (t < ntok && ch_ok) *reinterpret_cast<uint4*>(out + t * N + (lane & 3) * 8) = v;
   }
 }
@@ -307,6 +311,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   uint8_t* smA = smem;
   uint8_t* smB = smem + Cfg::OFF_B;
   float* ring = reinterpret_cast<float*>(smem + Cfg::OFF_SC);
+  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_VALID);
   int* lo = reinterpret_cast<int*>(smem + Cfg::OFF_LO);
   int* cum = reinterpret_cast<int*>(smem + Cfg::OFF_CUM);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
@@ -577,6 +582,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M)) tok[i] = r;
           }
         }
+        // word i of a slot's bits: which of columns 32 i .. 32 i + 31 have a token
+        auto write_valid = [&]() {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const uint32_t has = __ballot_sync(0xffffffffu, tok[i] >= 0);
+            if (lane == 0) valid[slot * NV + i] = has;
+          }
+        };
         auto next_slot = [&]() {
           if (++slot == Cfg::SSLOTS) { slot = 0; phase ^= 1u; }
         };
@@ -587,6 +600,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (!warp_wait_bounded(sfree + slot, phase ^ 1u, abort_flag)) { ok = false; break; }
 #pragma unroll
           for (int i = 0; i < NV; ++i) ring[slot * BT + i * 32 + lane] = v[i];
+          write_valid();
           __syncwarp();
           if (lane == 0) mbar_arrive(sfull + slot);
           next_slot();
@@ -622,6 +636,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               to[2 * BT + i * 32] = __fmul_rn(v[i].z, w.z);
               to[3 * BT + i * 32] = __fmul_rn(v[i].w, w.w);
             }
+            if (b + 4 >= nk) write_valid();  // the epilogue reads them with the tile's last slot
             __syncwarp();
             if (lane == 0) mbar_arrive(sfull + slot);
             kb += 8;
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     auto combine = [&](auto&& value, auto&& add) {
       uint8_t* mine = smem + Cfg::OFF_PART + q * 4096 + lane * 16;
       if (pair > 0) {
-        const uint32_t to = mapa_shared(smem_u32(mine) + (pair - 1) * Cfg::PART_BYTES, rank);
+        const uint32_t to = mapa_shared(smem_u32(mine + (pair - 1) * Cfg::PART_BYTES), rank);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           st_cluster_v4(to + i * 512, value(4 * i), value(4 * i + 1), value(4 * i + 2), value(4 * i + 3));
@@ -707,6 +722,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               if (pair > 0 || !ok) break;
             }
           }
+          const uint32_t bits = valid[r * (BT / 32) + (c >> 5)];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t pk[2][4];
@@ -722,7 +738,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               }
             }
             grouped_store<Cfg::PITCH>(st, out + (c + i * 16) * N, N, lane, pk,
-                                      tile.nrows - c - i * 16, ch_ok);
+                                      tile.nrows - c - i * 16, bits >> (i * 16), ch_ok);
           }
         }
         release(a);
@@ -770,6 +786,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (has0) add(acc[0], v[0], f[0]);
           if (has1) add(acc[1], v[1], f[1]);
         };
+        auto next_scales = [&]() {  // done with the slot's vectors
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfree + sslot);
+          if (++sslot == Cfg::SSLOTS) { sslot = 0; sphase ^= 1u; }
+        };
         const uint32_t l1 = local + (nk > 1 ? 1 : 0);
         if (!prompt_wait(tfull + l1 % NACC, l1 / NACC & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -791,11 +812,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             tc_fence_after();
             load_block(l2);
           }
-          if ((kb & 2) || !more) {  // done with the slot's vectors
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sfree + sslot);
-            if (++sslot == Cfg::SSLOTS) { sslot = 0; sphase ^= 1u; }
-          }
+          if ((kb & 2) && more) next_scales();
           local += two ? 2 : 1;
           if (more && !early) {
             if (!prompt_wait(tfull + l3 % NACC, l3 / NACC & 1u, abort_flag)) { ok = false; break; }
@@ -804,6 +821,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         if (!ok) break;
+        // the last slot is held until the stores: its bits, read earlier, cost a spill
+        const uint32_t* bits = valid + sslot * (BT / 32) + (col0 >> 5);
         if constexpr (Cfg::SPLIT) {
           if (split > 1 && has0) {
             float sum[32];
@@ -832,8 +851,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                                        __uint_as_float(static_cast<uint32_t>(x >> 32)));
               }
             grouped_store<Cfg::PITCH>(st, out + (col0 + i * 16) * N, N, lane, pk,
-                                      tile.nrows - col0 - i * 16, ch_ok);
+                                      tile.nrows - col0 - i * 16, bits[i >> 1] >> (16 * (i & 1)), ch_ok);
           }
+        next_scales();
       }
     }
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");  // a wait may have given up before it
