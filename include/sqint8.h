@@ -274,7 +274,7 @@ sq_status sq_silu_mul_quant_fp8(const void* gate_up_bf16, const float* inv_smoot
  *   acc[n] = sum_k q_a[m,k] * q_w[e,n,k] (exact int32),
  *   y[t,n] = bf16_rne((f32(acc) * s_tok[m]) * s_ch[e,n]).
  * q_a int8 [M,K], s_tok fp32 [M], q_w int8 [E,N,K], s_ch fp32 [E,N], y BF16
- * [T,N].  A rows[t] outside [0, M) is a padding row: y[t,:] = 0.  Rows before
+ * [T,N], M >= 1.  A rows[t] outside [0, M) is a padding row: y[t,:] = 0.  Rows before
  * offsets[0] and from offsets[E] on are left as they were.  Offsets outside
  * [0, T] or decreasing are held to the range and to the largest before them, so
  * they reach no memory outside the buffers.  E <= 1024, N % 16 == 0, K % 128 ==
@@ -286,7 +286,9 @@ sq_status w8a8_grouped_mm(const int8_t* q_a, const float* s_tok, const int32_t* 
                           void* stream);
 
 /* FP8 block-scaled products grouped by expert: rows and offsets as above, the
- * arithmetic of fp8_block_mm.  q_a E4M3 [M,K], s_a fp32 [M, K/128], q_w E4M3
+ * arithmetic of fp8_block_mm (a call of at most 32 rows may sum K in 2 or 4
+ * contiguous parts, each in order, and add the parts in order: the same from run
+ * to run, but a row's last bits may differ from those of a larger call).  q_a E4M3 [M,K], s_a fp32 [M, K/128], q_w E4M3
  * [E,N,K], s_w fp32 [E, N/128, K/128] (sq_quant_fp8_block of each expert's
  * weights); N % 128 == 0. */
 sq_status fp8_block_grouped_mm(const uint8_t* q_a, const float* s_a, const int32_t* rows,

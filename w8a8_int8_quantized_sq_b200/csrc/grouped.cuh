@@ -64,7 +64,7 @@ struct GroupedArgs {
   int T, M, E, N;
   int kb_total;            // K / 128
   int tiles_n;             // ceil(N / 256)
-  int split;               // CTA pairs that share a tile's K (1 unless the tiles are 32 tokens wide)
+  int split;               // CTA pairs that share a tile's K: 2 or 4 with tiles of 32 tokens, else 1
 };
 
 // Tensor maps of the token rows: boxes of 16, 32, 64 and 128 rows, of which a tile
@@ -77,17 +77,26 @@ struct GroupedMaps {
 };
 
 // BT: most tokens per tile.  256 (INT8, two accumulators for a tile each) and 128 (FP8,
-// four for a K block each) fill the tensor memory.  32 is for calls of at most 32 rows,
-// whose few tiles would leave most SMs idle (an SM pair reads about 100 bytes/ns, and
-// a deeper ring does not change that): there a tile's K may be split over the 2 or 4
-// CTA pairs of one cluster.  The other pairs' partial sums meet in the first's shared
+// four for a K block each) fill the tensor memory.  32 is for calls of at most 32 rows
+// with so few tiles that most SMs would idle (an SM pair reads about 100 bytes/ns, and
+// a deeper ring does not change that): there a tile's K is split over the 2 or 4 CTA
+// pairs of one cluster.  The other pairs' partial sums meet in the first's shared
 // memory and are added in the order of K, so the answer does not depend on timing.
+// Measured with N = 2048, split and on one pair, us:
+//   1 row (8 tiles, 4 pairs, 2, 1),   K = 2048: INT8 8.0, 8.1, 9.0; FP8 8.9, 8.9, 9.9
+//                                     K = 5120: INT8 9.5, 11.3, 15.3; FP8 10.7, 12.6, 17.5
+//   2 rows in 2 experts (16 tiles),   K = 2048: INT8 8.3, 9.0; FP8 9.2, 10.0
+//                                     K = 5120: INT8 11.4, 15.2; FP8 12.8, 17.5
+//   4 rows in 4 experts (32 tiles),   K = 2048: INT8 9.2, 9.1; FP8 10.3, 10.2
+//                                     K = 5120: INT8 13.6, 16.0; FP8 15.0, 18.3
+// With more tiles than resident clusters the 32-token tiles on one pair are no faster
+// than the wide ones (8 to 64 rows: 0 to 4 % slower), so those run the wide ones.
 template <bool F8_, int BT_>
 struct GroupedCfg {
   static constexpr bool F8 = F8_;
   static constexpr int BT = BT_;
   static constexpr int NACC = F8 ? 4 : 2;        // accumulators (BT tensor-memory columns each)
-  static constexpr bool SPLIT = BT == 32;        // K may be split over the cluster's pairs
+  static constexpr bool SPLIT = BT == 32;        // K is split over the cluster's pairs
   static constexpr int STAGES = BT == 32 || F8 ? 8 : 6;
   static constexpr int PART_BYTES = 128 * 32 * 4;  // one CTA's partial sums of a split tile
   static constexpr int A_BYTES = 128 * 128;      // weights staged by each CTA per K block
@@ -716,11 +725,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           tmem_frags_async(src + c, v);
           tmem_frags_wait(v);
           if constexpr (Cfg::SPLIT) {
-            if (split > 1) {
-              ok = combine([&](int i) { return v[i >> 4][i & 15]; },
-                           [&](int i, uint32_t x) { v[i >> 4][i & 15] += x; });
-              if (pair > 0 || !ok) break;
-            }
+            ok = combine([&](int i) { return v[i >> 4][i & 15]; },
+                         [&](int i, uint32_t x) { v[i >> 4][i & 15] += x; });
+            if (pair > 0 || !ok) break;
           }
           const uint32_t bits = valid[r * (BT / 32) + (c >> 5)];
 #pragma unroll
@@ -824,7 +831,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // the last slot is held until the stores: its bits, read earlier, cost a spill
         const uint32_t* bits = valid + sslot * (BT / 32) + (col0 >> 5);
         if constexpr (Cfg::SPLIT) {
-          if (split > 1 && has0) {
+          if (has0) {
             float sum[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i)

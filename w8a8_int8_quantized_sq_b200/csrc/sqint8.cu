@@ -804,13 +804,14 @@ sq_status silu_mul_quant(const void* gate_up, const float* inv_smooth, int fmt, 
 // Clusters of `split` CTA pairs that the device holds at once (asked once per device),
 // 0 if it cannot be told.
 template <class Cfg>
-int grouped_clusters(int split, int smem) {
+int grouped_clusters(int split) {
   static std::atomic<int> cap[64][3];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::atomic<int>& slot = cap[dev][split / 2];
   int mc = slot.load(std::memory_order_acquire);
   if (mc > 0) return mc;
+  const int smem = Cfg::smem_bytes();
   if (cudaFuncSetAttribute(grouped_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return 0;
@@ -830,56 +831,54 @@ int grouped_clusters(int split, int smem) {
   return mc;
 }
 
+// Most tiles the offsets can give: each group of rows ends in at most one partial tile.
 template <class Cfg>
-sq_status launch_grouped(const void* q_a, const float* s_a, const int32_t* rows, const void* q_w,
-                         const float* s_w, const int32_t* offsets, void* y, int64_t T, int64_t M,
-                         int64_t E, int64_t N, int64_t K, cudaStream_t st) {
-  const uint64_t k = static_cast<uint64_t>(K);
+int64_t grouped_tiles(const GroupedArgs& g) {
+  return static_cast<int64_t>((g.T < g.E ? g.T : g.E) + g.T / Cfg::BT) * g.tiles_n;
+}
+
+// On clusters of g.split pairs, at most mc of them.
+template <class Cfg>
+sq_status launch_grouped(const void* q_a, const void* q_w, const GroupedArgs& g, int mc, cudaStream_t st) {
+  const uint64_t k = static_cast<uint64_t>(g.kb_total) * 128;
+  const uint64_t m = static_cast<uint64_t>(g.M);
   CUtensorMap tw;
   GroupedMaps tx{};
-  if (!make_map(&tw, q_w, false, k, static_cast<uint64_t>(E * N), 128, 128)) return SQ_ERR_CUDA;
-  if (rows) {
-    if (!make_map(&tx.m[0], q_a, false, k, static_cast<uint64_t>(M), 128, 1)) return SQ_ERR_CUDA;
+  if (!make_map(&tw, q_w, false, k, static_cast<uint64_t>(g.E) * static_cast<uint64_t>(g.N), 128, 128))
+    return SQ_ERR_CUDA;
+  if (g.rows) {
+    if (!make_map(&tx.m[0], q_a, false, k, m, 128, 1)) return SQ_ERR_CUDA;
   } else {
     // boxes up to the half of the largest tile that T rows can make
-    const int64_t most = T < Cfg::BT ? T : Cfg::BT;
+    const int most = g.T < Cfg::BT ? g.T : Cfg::BT;
     for (int i = 0; i < 4 && (i == 0 || (16 << (i - 1)) < (most + 31) / 32 * 16); ++i)
-      if (!make_map(&tx.m[i], q_a, false, k, static_cast<uint64_t>(M), 128, 16u << i))
-        return SQ_ERR_CUDA;
+      if (!make_map(&tx.m[i], q_a, false, k, m, 128, 16u << i)) return SQ_ERR_CUDA;
   }
-  // most tiles the offsets can give: each group of rows ends in at most one partial tile
-  const int64_t tiles_n = (N + 255) / 256;
-  const int64_t tiles = ((T < E ? T : E) + T / Cfg::BT) * tiles_n;
-  const int smem = Cfg::smem_bytes();
-  // A tile's K over 4 or 2 pairs where every tile can have a resident cluster of its own
-  // and a pair keeps two K blocks or more.  (2 rows, K = N = 2048: see grouped.cuh.)
-  int split = 1, mc = 0;
-  if constexpr (Cfg::SPLIT) {
-    for (split = 4; split > 1; split /= 2) {
-      if (K / 128 < 2 * split) continue;
-      mc = grouped_clusters<Cfg>(split, smem);
+  const int64_t tiles = grouped_tiles<Cfg>(g);
+  const int clusters = tiles < mc ? static_cast<int>(tiles) : mc;
+  return launch_dependent(grouped_kernel<Cfg>, static_cast<unsigned>(2 * g.split * clusters),
+                          Cfg::THREADS, Cfg::smem_bytes(), st, 2 * g.split, tw, tx, g);
+}
+
+// A tile's K over 4 or 2 pairs where every tile can have a resident cluster of its own
+// and a pair keeps two K blocks or more; else one pair per tile.  (Both measured, with
+// 32-token tiles on one pair too, beside the kernel.)
+template <bool F8>
+sq_status launch_grouped(const void* q_a, const void* q_w, GroupedArgs g, cudaStream_t st) {
+  using Narrow = GroupedCfg<F8, 32>;
+  using Wide = GroupedCfg<F8, F8 ? 128 : 256>;
+  if (g.T <= Narrow::BT) {
+    for (g.split = 4; g.split > 1; g.split /= 2) {
+      if (g.kb_total < 2 * g.split) continue;
+      const int mc = grouped_clusters<Narrow>(g.split);
       if (mc <= 0) return SQ_ERR_CUDA;
-      if (tiles <= mc) break;
+      if (grouped_tiles<Narrow>(g) <= mc) return launch_grouped<Narrow>(q_a, q_w, g, mc, st);
     }
   }
-  if (split == 1) mc = grouped_clusters<Cfg>(1, smem);
+  g.split = 1;
+  const int mc = grouped_clusters<Wide>(1);
   if (mc <= 0) return SQ_ERR_CUDA;
-  GroupedArgs g{};
-  g.offsets = offsets;
-  g.rows = rows;
-  g.s_a = s_a;
-  g.s_w = s_w;
-  g.out = static_cast<__nv_bfloat16*>(y);
-  g.T = static_cast<int>(T);
-  g.M = static_cast<int>(M);
-  g.E = static_cast<int>(E);
-  g.N = static_cast<int>(N);
-  g.kb_total = static_cast<int>(K / 128);
-  g.tiles_n = static_cast<int>(tiles_n);
-  g.split = split;
-  const int clusters = tiles < mc ? static_cast<int>(tiles) : mc;
-  return launch_dependent(grouped_kernel<Cfg>, static_cast<unsigned>(2 * split * clusters),
-                          Cfg::THREADS, smem, st, 2 * split, tw, tx, g);
+  return launch_grouped<Wide>(q_a, q_w, g, mc, st);
 }
 
 sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* rows,
@@ -900,10 +899,20 @@ sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* 
   if (!aligned16(q_a) || !aligned16(s_a) || !aligned16(q_w) || !aligned16(s_w) ||
       !aligned16(offsets) || !aligned16(y) || (rows && !aligned16(rows)))
     return SQ_ERR_ALIGN;
+  GroupedArgs g{};
+  g.offsets = offsets;
+  g.rows = rows;
+  g.s_a = s_a;
+  g.s_w = s_w;
+  g.out = static_cast<__nv_bfloat16*>(y);
+  g.T = static_cast<int>(T);
+  g.M = static_cast<int>(M);
+  g.E = static_cast<int>(E);
+  g.N = static_cast<int>(N);
+  g.kb_total = static_cast<int>(K / 128);
+  g.tiles_n = static_cast<int>((N + 255) / 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto launch = f8 ? (T <= 32 ? launch_grouped<GroupedCfg<true, 32>> : launch_grouped<GroupedCfg<true, 128>>)
-                   : (T <= 32 ? launch_grouped<GroupedCfg<false, 32>> : launch_grouped<GroupedCfg<false, 256>>);
-  return launch(q_a, s_a, rows, q_w, s_w, offsets, y, T, M, E, N, K, st);
+  return f8 ? launch_grouped<true>(q_a, q_w, g, st) : launch_grouped<false>(q_a, q_w, g, st);
 }
 
 }  // namespace
