@@ -35,20 +35,22 @@
 // What bounds it, measured on one B200 (INT8 codes of normal values unless said):
 //   INT8, 8 experts x 1024 rows, N = 8192: K = 5120 225-232 us (3000 TOPS; 4030 with zero
 //     codes, so the power limit, not the pipeline), K = 2048 98-102 us (2750 TOPS).
-//   INT8, 32768 rows over 64 experts, K = N = 2048: 123-127 us (132-137 us gathered; 104 us
+//   INT8, 32768 rows over 64 experts, K = N = 2048: 123-127 us, gathered 127-130 us (104 us
 //     with zero codes).  Token tiles that are not full and the uneven last wave cost the rest.
-//   INT8, 128 rows over 64 experts, K = 2048, N = 1536: 36 us, 5.5 TB/s of weights.
-//   FP8, 8198 rows over 8 experts, K = 5120, N = 2048: 138 us, 1240 TOPS (148 us
-//     gathered).  The epilogue's own chain per K block (tensor-memory reads of 64 bytes
-//     per clock and SM quadrant, releases, fused multiply-adds) takes 780 cycles; with
-//     the promotion left out the call takes 115 us, the loads and MMAs alone 87 us.
+//   INT8, 128 rows over 64 experts, K = 2048, N = 1536: 34 us, 5.3 TB/s in all.
+//   FP8, 8198 rows over 8 experts, K = 5120, N = 2048: 119 us, 1440 TOPS (127 us
+//     gathered); the loads and MMAs alone take 87 us.  The epilogue's own chain per K block
+//     (tensor-memory reads of 64 bytes per clock and SM quadrant, releases, fused
+//     multiply-adds) bounds it.  With branches on the warp's chunks inside the K loop and
+//     both chunks read before either was added it took 139 us.
 //     Slower variants: lanes as channels with broadcast scales (220 us), 16 epilogue
 //     warps of 32 columns (143 us but decode 6 % slower), 192- and 256-token tiles with two
 //     accumulators (240-400 us), waits with the suspend hint (240 us).
-//   FP8, 222 rows over 64 experts, K = 1408, N = 2048: 37 us, 5.0 TB/s of weights.
+//   FP8, 222 rows over 64 experts, K = 1408, N = 2048: 34 us, 5.4 TB/s in all.
 //   Token rows copied by cp.async threads instead of TMA ran 2-3 times slower (the
 //   proxy fences wait for every copy in flight).
 #pragma once
+#include <type_traits>
 #include "gemm3.cuh"
 
 namespace sq {
@@ -527,14 +529,22 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       __syncwarp();
     } else if (warp >= 2 + Cfg::NS) {
       // ---------------------------------------------------- gathered tokens
-      // Each lane fetches four rows of a stage; lane l of warp w takes rows 4 (NG l +
-      // w) and up, so that the warps share the loads evenly.  A load takes its warp
-      // about 80 cycles to issue: from one warp alone they made the prefill of
-      // 32768 rows over 64 experts, K = N = 2048, take 346 us, from four 152 us,
-      // from eight 140 us.
+      // Warps take the stages in turn, NG / 4 of them to a stage, and each lane fetches four
+      // rows; the warps of a stage share the loads evenly.  A load takes its warp about
+      // 80 cycles to issue and a stage's wait over 100, so the loads are spread over
+      // warps and the waits are not repeated by all of them: the prefill of 32768 rows
+      // over 64 experts, K = N = 2048, took 346 us with one warp, 152 with four and 138
+      // with eight on every stage, 130 and 127 us with eight on every second and fourth.
       if (g.rows) {
         const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
-        const int j = (lane * Cfg::NG + warp - 2 - Cfg::NS) * 4;
+        constexpr int TURNS = 4, WARPS = Cfg::NG / TURNS;  // warps of a stage
+        // A parity wait tells a phase from the next only.  Before fill f (which waits until fill
+        // f - STAGES is consumed) this warp saw fill f - TURNS - STAGES consumed, and so
+        // fill f - 2 STAGES: the wait cannot take that phase for its own.
+        static_assert(TURNS <= STAGES && WARPS * TURNS == Cfg::NG, "gather warps");
+        const int gw = warp - 2 - Cfg::NS;
+        const int j = (lane * WARPS + gw / TURNS) * 4;
+        int skip = gw % TURNS;  // stages until this warp's next
         GroupedWalk walk(lo, cum, g.tiles_n);
         uint32_t stage = 0, phase = 0;
         bool ok = true;
@@ -552,14 +562,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           int4 r4 = make_int4(g.M, g.M, g.M, g.M);
           if (mine) r4 = make_int4(token(0), token(1), token(2), token(3));
           for (int kb = 0; kb < nk; ++kb) {
-            if (!warp_wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
-              ok = false;
-              break;
+            if (skip == 0) {
+              if (!warp_wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
+                ok = false;
+                break;
+              }
+              if (mine)
+                tma_gather4_pair(smB + stage * Cfg::B_BYTES + j * 128, &tmX.m[0], (k0 + kb) * 128, r4,
+                                 full_leader + stage * 8);
+              __syncwarp();
             }
-            if (mine)
-              tma_gather4_pair(smB + stage * Cfg::B_BYTES + j * 128, &tmX.m[0], (k0 + kb) * 128, r4,
-                               full_leader + stage * 8);
-            __syncwarp();
+            skip = skip == 0 ? TURNS - 1 : skip - 1;
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -771,62 +784,79 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               for (int r = 2 * i; r < 2 * i + 2; ++r)
                 x[h][r] = fma2(y[h][2 * r], y[h][2 * r + 1], f[i], x[h][r]);
         };
-        // K blocks are taken in pairs on one poll (a poll takes over 100 cycles even when it
-        // succeeds; commits arrive in order, so the second is complete after the
-        // first), and a block's partials are requested as soon as the registers are free.
-        auto load_scales = [&](int kb) {
-          const float* s = ring + (sslot * Cfg::SV + (kb & 3)) * BT + (has0 ? col0 : 0) + (lane & 3) * 2;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[0][i] = *reinterpret_cast<const uint64_t*>(s + i * 8);
-            if constexpr (BT > 32) f[1][i] = *reinterpret_cast<const uint64_t*>(s + 32 + i * 8);
-          }
-        };
-        auto load_block = [&](uint32_t l) {
-          if (has0) tmem_frags_async(src + l % NACC * BT, v[0]);
-          if (has1) tmem_frags_async(src + l % NACC * BT + 32, v[1]);
-        };
-        auto add_block = [&](uint32_t l) {
-          tmem_frags_wait(v[0]);
-          tmem_frags_wait(v[1]);
-          release(l % NACC);  // the K block is in registers
-          if (has0) add(acc[0], v[0], f[0]);
-          if (has1) add(acc[1], v[1], f[1]);
-        };
         auto next_scales = [&]() {  // done with the slot's vectors
           __syncwarp();
           if (lane == 0) mbar_arrive(sfree + sslot);
           if (++sslot == Cfg::SSLOTS) { sslot = 0; sphase ^= 1u; }
         };
-        const uint32_t l1 = local + (nk > 1 ? 1 : 0);
-        if (!prompt_wait(tfull + l1 % NACC, l1 / NACC & 1u, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        load_block(local);
-        for (int kb = 0; kb < nk; kb += 2) {
-          if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) { ok = false; break; }
-          load_scales(kb);
-          const bool two = kb + 1 < nk, more = kb + 2 < nk;
-          const uint32_t l2 = local + 2, l3 = kb + 3 < nk ? local + 3 : l2;  // the next pair
-          const bool polled = more && prompt_try_wait(smem_u32(tfull + l3 % NACC), l3 / NACC & 1u);
-          add_block(local);
-          if (two) {
-            load_block(local + 1);
-            load_scales(kb + 1);
-            add_block(local + 1);
+        // The tile's K blocks for a warp with this many chunks, without a branch on
+        // them inside the loop.  K blocks are taken in pairs on one poll (a poll takes over
+        // 100 cycles even when it succeeds; commits arrive in order, so the second is
+        // complete after the first).  With two chunks, one's partials are read while the
+        // other's are added.  False: a wait gave up.
+        auto k_blocks = [&](auto chunks) -> bool {
+          constexpr int CH = decltype(chunks)::value;
+          auto load_scales = [&](int kb) {
+            const float* s = ring + (sslot * Cfg::SV + (kb & 3)) * BT + col0 + (lane & 3) * 2;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[c][i] = *reinterpret_cast<const uint64_t*>(s + c * 32 + i * 8);
+          };
+          auto load = [&](uint32_t l, int c) {
+            if (c < CH) tmem_frags_async(src + l % NACC * BT + 32 * c, v[c]);
+          };
+          // one K block, whose first chunk is on its way
+          auto block = [&](uint32_t l) {
+            if constexpr (CH > 0) tmem_frags_wait(v[0]);
+            if constexpr (CH == 2) load(l, 1);
+            else release(l % NACC);
+            if constexpr (CH > 0) add(acc[0], v[0], f[0]);
+            if constexpr (CH == 2) {
+              tmem_frags_wait(v[1]);
+              release(l % NACC);
+            }
+          };
+          auto rest = [&]() {  // after the next block's load
+            if constexpr (CH == 2) add(acc[1], v[1], f[1]);
+          };
+          const uint32_t l1 = local + (nk > 1 ? 1 : 0);
+          if (!prompt_wait(tfull + l1 % NACC, l1 / NACC & 1u, abort_flag)) return false;
+          tc_fence_after();
+          load(local, 0);
+          for (int kb = 0; kb < nk; kb += 2) {
+            if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) return false;
+            load_scales(kb);
+            const bool two = kb + 1 < nk, more = kb + 2 < nk;
+            const uint32_t l2 = local + 2, l3 = kb + 3 < nk ? local + 3 : l2;  // the next pair
+            block(local);
+            const bool polled = more && prompt_try_wait(smem_u32(tfull + l3 % NACC), l3 / NACC & 1u);
+            if (two) {
+              load(local + 1, 0);
+              rest();
+              load_scales(kb + 1);
+              block(local + 1);
+            }
+            const bool early = __all_sync(0xffffffffu, polled);
+            if (early) {
+              tc_fence_after();
+              load(l2, 0);
+            }
+            rest();
+            if ((kb & 2) && more) next_scales();
+            local += two ? 2 : 1;
+            if (more && !early) {
+              if (!prompt_wait(tfull + l3 % NACC, l3 / NACC & 1u, abort_flag)) return false;
+              tc_fence_after();
+              load(l2, 0);
+            }
           }
-          const bool early = __all_sync(0xffffffffu, polled);
-          if (early) {
-            tc_fence_after();
-            load_block(l2);
-          }
-          if ((kb & 2) && more) next_scales();
-          local += two ? 2 : 1;
-          if (more && !early) {
-            if (!prompt_wait(tfull + l3 % NACC, l3 / NACC & 1u, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            load_block(l2);
-          }
+          return true;
+        };
+        if constexpr (BT > 32) {
+          if (has1) ok = k_blocks(std::integral_constant<int, 2>());
         }
+        if (!has1) ok = has0 ? k_blocks(std::integral_constant<int, 1>()) : k_blocks(std::integral_constant<int, 0>());
         if (!ok) break;
         // the last slot is held until the stores: its bits, read earlier, cost a spill
         const uint32_t* bits = valid + sslot * (BT / 32) + (col0 >> 5);
