@@ -288,9 +288,9 @@ sq_status w8a8_grouped_mm(const int8_t* q_a, const float* s_tok, const int32_t* 
 /* FP8 block-scaled products grouped by expert: rows and offsets as above, the
  * arithmetic of fp8_block_mm (a call of at most 32 rows may sum K in 2 or 4
  * contiguous parts, each in order, and add the parts in order: the same from run
- * to run, but a row's last bits may differ from those of a larger call).  q_a E4M3 [M,K], s_a fp32 [M, K/128], q_w E4M3
- * [E,N,K], s_w fp32 [E, N/128, K/128] (sq_quant_fp8_block of each expert's
- * weights); N % 128 == 0. */
+ * to run, but a row's last bits may differ from those of a larger call).  q_a
+ * E4M3 [M,K], s_a fp32 [M, K/128], q_w E4M3 [E,N,K], s_w fp32 [E, N/128, K/128]
+ * (sq_quant_fp8_block of each expert's weights); N % 128 == 0. */
 sq_status fp8_block_grouped_mm(const uint8_t* q_a, const float* s_a, const int32_t* rows,
                                const uint8_t* q_w, const float* s_w, const int32_t* offsets,
                                void* y_bf16, int64_t T, int64_t M, int64_t E, int64_t N, int64_t K,

@@ -35,9 +35,9 @@
 // What bounds it, measured on one B200 (INT8 codes of normal values unless said):
 //   INT8, 8 experts x 1024 rows, N = 8192: K = 5120 225-232 us (3000 TOPS; 4030 with zero
 //     codes, so the power limit, not the pipeline), K = 2048 98-102 us (2750 TOPS).
-//   INT8, 32768 rows over 64 experts, K = N = 2048: 123-127 us, gathered 127-130 us (104 us
+//   INT8, 32768 rows over 64 experts, K = N = 2048: 122-126 us, gathered 124-128 us (104 us
 //     with zero codes).  Token tiles that are not full and the uneven last wave cost the rest.
-//   INT8, 128 rows over 64 experts, K = 2048, N = 1536: 34 us, 5.3 TB/s in all.
+//   INT8, 128 rows over 64 experts, K = 2048, N = 1536: 33.4 us, 5.3 TB/s in all.
 //   FP8, 8198 rows over 8 experts, K = 5120, N = 2048: 119 us, 1440 TOPS (127 us
 //     gathered); the loads and MMAs alone take 87 us.  The epilogue's own chain per K block
 //     (tensor-memory reads of 64 bytes per clock and SM quadrant, releases, fused
@@ -46,7 +46,7 @@
 //     Slower variants: lanes as channels with broadcast scales (220 us), 16 epilogue
 //     warps of 32 columns (143 us but decode 6 % slower), 192- and 256-token tiles with two
 //     accumulators (240-400 us), waits with the suspend hint (240 us).
-//   FP8, 222 rows over 64 experts, K = 1408, N = 2048: 34 us, 5.4 TB/s in all.
+//   FP8, 222 rows over 64 experts, K = 1408, N = 2048: 33.1 us, 5.5 TB/s in all.
 //   Token rows copied by cp.async threads instead of TMA ran 2-3 times slower (the
 //   proxy fences wait for every copy in flight).
 #pragma once
@@ -119,7 +119,8 @@ struct GroupedCfg {
   static constexpr int OFF_B = STAGES * A_BYTES;
   static constexpr int OFF_SC = OFF_B + STAGES * B_BYTES;
   static constexpr int OFF_VALID = OFF_SC + SSLOTS * SV * BT * 4;  // a bit per token and slot
-  static constexpr int OFF_ST = OFF_VALID + SSLOTS * ((BT / 32 * 4 + 15) & ~15);
+  static constexpr int OFF_INFO = OFF_VALID + SSLOTS * ((BT / 32 * 4 + 15) & ~15);  // a slot's tile
+  static constexpr int OFF_ST = OFF_INFO + SSLOTS * 16;
   static constexpr int OFF_PART = OFF_ST + NE * 16 * PITCH;
   static constexpr int OFF_LO = OFF_PART + (SPLIT ? 3 * PART_BYTES : 0);
   static constexpr int OFF_CUM = OFF_LO + (kMaxExperts + 1) * 4;
@@ -249,15 +250,27 @@ struct GroupedTile {
 
 // The tile list: expert by expert, channel tile by channel tile, the token tiles of a
 // weight tile next to each other.  cum[e] counts the token tiles of the experts before e.
+// Working a tile out takes a few hundred cycles, so only the warps that run ahead do (loads,
+// MMA, scales); the epilogue finds its tile with the first scales.  (With every warp
+// searching expert by expert, 1200 cycles of the epilogue's 13400 per tile, FP8 K = 2048,
+// went there: 4100 rows over 32 experts, K = 1024, 27.2 us against 26.0.)
 struct GroupedWalk {
   const int* lo;
   const int* cum;
-  int tiles_n, e;
-  __device__ __forceinline__ GroupedWalk(const int* lo_, const int* cum_, int tiles_n_)
-      : lo(lo_), cum(cum_), tiles_n(tiles_n_), e(0) {}
-  // tile t; t must not decrease from call to call
+  int tiles_n, E, e;
+  __device__ __forceinline__ GroupedWalk(const int* lo_, const int* cum_, int tiles_n_, int E_)
+      : lo(lo_), cum(cum_), tiles_n(tiles_n_), E(E_), e(0) {}
+  // tile t of the list, for the whole warp; t must not decrease from call to call
   __device__ __forceinline__ GroupedTile at(int t) {
-    while (t >= cum[e + 1] * tiles_n) ++e;
+    const int lane = threadIdx.x & 31;
+    for (;; e += 32) {  // the first expert whose tiles end after t, 32 at a time
+      const int next = min(e + 1 + lane, E);
+      const uint32_t after = __ballot_sync(0xffffffffu, cum[next] * tiles_n > t);
+      if (after) {
+        e += __ffs(after) - 1;
+        break;
+      }
+    }
     const int nt = cum[e + 1] - cum[e];
     const int i = t - cum[e] * tiles_n;
     const int r = lo[e + 1] - lo[e];
@@ -266,7 +279,7 @@ struct GroupedWalk {
     g.ct = i;
     g.row0 = lo[e];
     g.nrows = r;
-    if (nt > 1) {  // the divisions take a few hundred cycles, which short tiles would notice
+    if (nt > 1) {
       const int w = ((r + nt - 1) / nt + 31) & ~31;  // rows per token tile, at most BT
       g.ct = i / nt;
       const int tt = i - g.ct * nt;
@@ -323,6 +336,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   uint8_t* smB = smem + Cfg::OFF_B;
   float* ring = reinterpret_cast<float*>(smem + Cfg::OFF_SC);
   uint32_t* valid = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_VALID);
+  int4* info = reinterpret_cast<int4*>(smem + Cfg::OFF_INFO);
   int* lo = reinterpret_cast<int*>(smem + Cfg::OFF_LO);
   int* cum = reinterpret_cast<int*>(smem + Cfg::OFF_CUM);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
@@ -425,27 +439,30 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if constexpr (Cfg::F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::CONTROL_REGS));
     if (warp == 0) {
       // ------------------------------- weights, and tokens in row order (TMA)
-      if (lane == 0) {
-        const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
-        const uint64_t pol = policy_evict_normal();
-        GroupedWalk walk(lo, cum, g.tiles_n);
-        uint32_t stage = 0, phase = 0;
-        long long fills = 0;
-        bool ok = true;
-        for (int t = cluster; ok && t < num_tiles; t += nclusters) {
-          const GroupedTile tile = walk.at(t);
-          const int half = ((tile.nrows + 31) & ~31) >> 1;  // token rows staged by this CTA
-          const int w_row = tile.e * g.N + tile.ct * 256 + static_cast<int>(rank) * 128;
-          const int x_row = tile.row0 + static_cast<int>(rank) * half;
-          // the smallest box of 16 << box rows that holds the half
-          const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-          const uint32_t bytes = 2 * (Cfg::A_BYTES + (g.rows ? half : 16 << box) * 128);
+      const uint32_t full_leader = mapa_shared(smem_u32(full), lead);
+      const uint64_t pol = policy_evict_normal();
+      GroupedWalk walk(lo, cum, g.tiles_n, g.E);
+      uint32_t stage = 0, phase = 0;
+      long long fills = 0;
+      bool ok = true;
+      for (int t = cluster; ok && t < num_tiles; t += nclusters) {
+        const GroupedTile tile = walk.at(t);
+        const int n = (tile.nrows + 31) & ~31;
+        const int half = n >> 1;  // token rows staged by this CTA
+        const int w_row = tile.e * g.N + tile.ct * 256 + static_cast<int>(rank) * 128;
+        const int x_row = tile.row0 + static_cast<int>(rank) * half;
+        // the smallest box of 16 << box rows that holds the half
+        const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        const uint32_t bytes = 2 * (Cfg::A_BYTES + (g.rows ? half : 16 << box) * 128);
+        if (lane == 0) {
           for (int kb = 0; kb < nk; ++kb) {
             if (!wait_bounded(empty + stage, phase ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
-            if (leader) mbar_arrive_expect_tx(full + stage, bytes);
+            if (leader) {
+              mbar_arrive_expect_tx(full + stage, bytes);
+            }
             tma_load_2d_pair(smA + stage * Cfg::A_BYTES, &tmW, (k0 + kb) * 128, w_row,
                              full_leader + stage * 8, pol);
             if (!g.rows)
@@ -458,12 +475,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
           }
         }
-        if (leader) {
-          // the pair's copies (both CTAs' bytes count here) have all landed
-          for (int st = 0; st < STAGES; ++st) {
-            const long long n = fills / STAGES + (st < fills % STAGES ? 1 : 0);
-            if (n > 0) wait_drain(full + st, static_cast<uint32_t>((n - 1) & 1));
-          }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (lane == 0 && leader) {
+        // the pair's copies (both CTAs' bytes count here) have all landed
+        for (int st = 0; st < STAGES; ++st) {
+          const long long n = fills / STAGES + (st < fills % STAGES ? 1 : 0);
+          if (n > 0) wait_drain(full + st, static_cast<uint32_t>((n - 1) & 1));
         }
       }
       __syncwarp();
@@ -484,12 +502,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
       }
       if (leader) {
-        GroupedWalk walk(lo, cum, g.tiles_n);
+        GroupedWalk walk(lo, cum, g.tiles_n, g.E);
         uint32_t stage = 0, phase = 0, local = 0;
         bool ok = true;
         for (int t = cluster; ok && t < num_tiles; t += nclusters) {
-          const GroupedTile tile = walk.at(t);
-          const int n = (tile.nrows + 31) & ~31;
+          const int n = (walk.at(t).nrows + 31) & ~31;
           const uint32_t idesc = Cfg::F8 ? idesc_e4m3_f32_m256(n) : idesc_i8_s32_m256(n);
           uint32_t d = 0;
           for (int kb = 0; kb < nk; ++kb) {
@@ -545,7 +562,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int gw = warp - 2 - Cfg::NS;
         const int j = (lane * WARPS + gw / TURNS) * 4;
         int skip = gw % TURNS;  // stages until this warp's next
-        GroupedWalk walk(lo, cum, g.tiles_n);
+        GroupedWalk walk(lo, cum, g.tiles_n, g.E);
         uint32_t stage = 0, phase = 0;
         bool ok = true;
         for (int t = cluster; ok && t < num_tiles; t += nclusters) {
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // then loaded again gave four K blocks per L2 latency, and decode of 222
       // rows over 64 experts (K = 1408, N = 2048) took 55 us.
       constexpr int NV = BT / 32;
-      GroupedWalk walk(lo, cum, g.tiles_n);
+      GroupedWalk walk(lo, cum, g.tiles_n, g.E);
       uint32_t slot = 0, phase = 0;
       const uint32_t mine = warp - 2;  // FP8: the slots of this parity
       bool ok = true;
@@ -623,6 +640,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < NV; ++i) ring[slot * BT + i * 32 + lane] = v[i];
           write_valid();
+          if (lane == 0) info[slot] = make_int4(tile.row0, tile.nrows, tile.e, tile.ct);
           __syncwarp();
           if (lane == 0) mbar_arrive(sfull + slot);
           next_slot();
@@ -658,6 +676,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               to[2 * BT + i * 32] = __fmul_rn(v[i].z, w.z);
               to[3 * BT + i * 32] = __fmul_rn(v[i].w, w.w);
             }
+            if (b == 0 && lane == 0) info[slot] = make_int4(tile.row0, tile.nrows, tile.e, tile.ct);
             if (b + 4 >= nk) write_valid();  // the epilogue reads them with the tile's last slot
             __syncwarp();
             if (lane == 0) mbar_arrive(sfull + slot);
@@ -708,15 +727,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
       return true;
     };
-    GroupedWalk walk(lo, cum, g.tiles_n);
     uint32_t local = 0, sslot = 0, sphase = 0;
     bool ok = true;
     for (int t = cluster; ok && t < num_tiles; t += nclusters) {
-      const GroupedTile tile = walk.at(t);
+      if (!warp_wait_bounded(sfull + sslot, sphase, abort_flag)) break;
+      const int4 in = info[sslot];  // row0, nrows, e, ct
+      const GroupedTile tile = {in.z, in.w, in.x, in.y};
       const int n = (tile.nrows + 31) & ~31;
       const int ch = tile.ct * 256 + static_cast<int>(rank) * 128 + q * 32;  // this warp's channels
       const bool ch_ok = ch + (lane & 3) * 8 < g.N;
       __nv_bfloat16* out = g.out + static_cast<size_t>(tile.row0) * N + ch;
+      auto next_scales = [&]() {  // done with the slot's vectors
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfree + sslot);
+        if (++sslot == Cfg::SSLOTS) { sslot = 0; sphase ^= 1u; }
+      };
       if constexpr (!Cfg::F8) {
         float s_ch[4];  // of channels 8 k + lane / 4
 #pragma unroll
@@ -725,11 +750,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           s_ch[k] = c < g.N ? __ldcg(g.s_w + static_cast<size_t>(tile.e) * N + c) : 0.0f;
         }
         const uint32_t a = local % NACC, u = local / NACC;
-        const uint32_t r = local % Cfg::SSLOTS, ur = local / Cfg::SSLOTS;
-        const float* slot = ring + r * BT;
+        const float* slot = ring + sslot * BT;
         ++local;
-        if (!warp_wait_bounded(sfull + r, ur & 1u, abort_flag) ||
-            !warp_wait_bounded(tfull + a, u & 1u, abort_flag)) { ok = false; break; }
+        if (!warp_wait_bounded(tfull + a, u & 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t src = lanes + a * BT;
 #pragma unroll 1
@@ -742,7 +765,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                          [&](int i, uint32_t x) { v[i >> 4][i & 15] += x; });
             if (pair > 0 || !ok) break;
           }
-          const uint32_t bits = valid[r * (BT / 32) + (c >> 5)];
+          const uint32_t bits = valid[sslot * (BT / 32) + (c >> 5)];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t pk[2][4];
@@ -762,7 +785,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         release(a);
-        if (lane == 0) mbar_arrive(sfree + r);
+        next_scales();
       } else {
         // this warp's columns: 64 or, of a tile of at most 64, 32; in two chunks of 32
         const int wcol = n > 64 ? 64 : 32;
@@ -783,11 +806,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
               for (int r = 2 * i; r < 2 * i + 2; ++r)
                 x[h][r] = fma2(y[h][2 * r], y[h][2 * r + 1], f[i], x[h][r]);
-        };
-        auto next_scales = [&]() {  // done with the slot's vectors
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sfree + sslot);
-          if (++sslot == Cfg::SSLOTS) { sslot = 0; sphase ^= 1u; }
         };
         // The tile's K blocks for a warp with this many chunks, without a branch on
         // them inside the loop.  K blocks are taken in pairs on one poll (a poll takes over
@@ -825,6 +843,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           tc_fence_after();
           load(local, 0);
           for (int kb = 0; kb < nk; kb += 2) {
+            // (at kb = 0 for the second time: a branch around it cost more)
             if ((kb & 3) == 0 && !prompt_wait(sfull + sslot, sphase, abort_flag)) return false;
             load_scales(kb);
             const bool two = kb + 1 < nk, more = kb + 2 < nk;
