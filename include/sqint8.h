@@ -254,11 +254,11 @@ sq_status sq_add_rmsnorm_quant_fp8(const void* h_bf16, const void* residual_bf16
 /* Gated activation + SmoothQuant fold + dynamic INT8 quantisation, between an
  * expert's (or an MLP's) two products.  gate_up BF16 [T, 2K]: columns 0..K-1 are
  * the gate g, K..2K-1 the other half u.  Per row: a = g / (1 + exp(-g)) * u in
- * fp32 (within 2^-19 of the exact value, or 2^-40 |u| absolutely), v =
+ * fp32 (within 2^-20 of the exact value, or 2^-110 |u| absolutely), v =
  * a * inv_smooth[k] (inv_smooth fp32 [K], may be NULL: 1), then codes and scales
  * of v as in sq_add_rmsnorm_quant, per row (group == 0 or K) or per 128 columns
- * (group == 128).  K % 128 == 0,
- * K <= 24576.  Non-finite rows and the launch as for sq_add_rmsnorm_quant. */
+ * (group == 128).  K % 128 == 0, K <= 24576.  Non-finite rows and the launch as
+ * for sq_add_rmsnorm_quant. */
 sq_status sq_silu_mul_quant(const void* gate_up_bf16, const float* inv_smooth, int64_t group,
                             int8_t* q_i8, float* scales, int64_t T, int64_t K, void* stream);
 

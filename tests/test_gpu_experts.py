@@ -401,7 +401,7 @@ def check_silu(gu, inv, fmt, q, sc):
     T, K = gu.shape[0], gu.shape[1] // 2
     g, u = gu.double().chunk(2, 1)
     v = g * torch.sigmoid(g) * u
-    slack = v.abs() * 2.0 ** -19 + u.abs() * 2.0 ** -40  # the stated error of the activation
+    slack = v.abs() * 2.0 ** -20 + u.abs() * 2.0 ** -110  # the stated error of the activation
     if inv is not None:
         v, slack = v * inv.double(), slack * inv.double()
     per = K if fmt == "i8" else 128
