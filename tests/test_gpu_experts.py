@@ -666,6 +666,28 @@ def test_two_graphs_replayed_at_once():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_layer_run_in_inference_mode_and_from_threads():
+    """Under inference mode, and from two host threads on streams of their own."""
+    from concurrent.futures import ThreadPoolExecutor
+    a = layer_inputs(5, 8, 2, 512, 256, "i8", 117)
+    args = cuda(*a[:5], *a[5]["up"], *a[5]["down"])
+    want = run_layer(*args, "i8")
+    torch.cuda.synchronize()
+    with torch.inference_mode():
+        got = run_layer(*args, "i8")
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+    def many(_):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            outs = [run_layer(*args, "i8") for _ in range(20)]
+        stream.synchronize()
+        return all(torch.equal(x, w) for o in outs for x, w in zip(o, want))
+
+    with ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(many, range(2)))
+
+
 # ------------------------------------------------------------------ large and many
 
 def test_grouped_i8_thousand_experts():
@@ -707,6 +729,27 @@ def test_grouped_weights_past_32_bits():
     ref = i8_reference(q_a.cpu(), s_a.cpu(), q_w[E - 2:].cpu(), s_w[E - 2:].cpu(),
                        torch.tensor([0, 7, 40]), None, torch.zeros(40, N, dtype=torch.bfloat16))
     assert_bits(y, ref, "y")
+
+
+@pytest.mark.parametrize("kind", ["i8", "fp8"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_tokens_past_32_bits(kind, gather):
+    """More than 2^31 bytes of tokens: rows at the end, by index and in order."""
+    M, N, K = 530_001, 128, 4096
+    c = (i8_case if kind == "i8" else fp8_case)([64, 0], N, K, False, 136)
+    mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+    q_a, s_a, q_w, s_w = cuda(*c[:4])
+    big = torch.zeros(M, K, dtype=q_a.dtype, device="cuda")
+    big_s = torch.zeros(M, *s_a.shape[1:], device="cuda")
+    big[-64:], big_s[-64:] = q_a, s_a
+    off = torch.tensor([0, 30, 64], dtype=torch.int32, device="cuda")
+    want = mm(q_a, s_a, q_w, s_w, off)
+    if gather:
+        rows = torch.arange(M - 64, M, dtype=torch.int32, device="cuda")
+        y = mm(big, big_s, q_w, s_w, off, rows=rows)
+    else:
+        y = mm(big, big_s, q_w, s_w, off + torch.tensor([M - 64], dtype=torch.int32, device="cuda"))[-64:]
+    assert torch.equal(y, want)
 
 
 @pytest.mark.parametrize("fmt", ["i8", "fp8"])
