@@ -688,6 +688,30 @@ def test_layer_run_in_inference_mode_and_from_threads():
         assert all(pool.map(many, range(2)))
 
 
+@pytest.mark.parametrize("M", [3, 2000])
+@pytest.mark.parametrize("fmt", ["i8", "i8_group", "fp8"])
+def test_outputs_of_one_call_are_apart(fmt, M):
+    """Aligned, not overlapping (small calls' outputs share an allocation), each with its own
+    values after the others have been written and freed."""
+    h = torch.randn(M, 768, generator=gen(118)).bfloat16().cuda()
+    gamma = torch.rand(768, device="cuda") + 0.25
+    for call in (lambda: call_norm(h, h, gamma, fmt), lambda: call_silu(h, None, fmt)):
+        want = [t.clone() for t in call()]
+        outs = list(call())
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in outs)
+        assert all(lo % 16 == 0 for lo, _ in spans)
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        for i in range(len(outs)):
+            for t in outs[:i]:
+                t.zero_()
+            assert torch.equal(outs[i], want[i])
+        last = outs.pop()
+        del outs, t
+        torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(7)
+        call()
+        assert torch.equal(last, want[-1])
+
+
 # ------------------------------------------------------------------ large and many
 
 def test_grouped_i8_thousand_experts():
