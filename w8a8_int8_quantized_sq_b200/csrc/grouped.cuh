@@ -122,7 +122,8 @@ struct GroupedCfg {
   static constexpr int OFF_INFO = OFF_VALID + SSLOTS * ((BT / 32 * 4 + 15) & ~15);  // a slot's tile
   static constexpr int OFF_ST = OFF_INFO + SSLOTS * 16;
   static constexpr int OFF_PART = OFF_ST + NE * 16 * PITCH;
-  static constexpr int OFF_LO = OFF_PART + (SPLIT ? 3 * PART_BYTES : 0);
+  static constexpr int OFF_ROWS = OFF_PART + (SPLIT ? 3 * PART_BYTES : 0);
+  static constexpr int OFF_LO = OFF_ROWS + (SPLIT ? BT * 4 : 0);
   static constexpr int OFF_CUM = OFF_LO + (kMaxExperts + 1) * 4;
   static constexpr int OFF_BAR = (OFF_CUM + (kMaxExperts + 1) * 4 + 7) & ~7;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * NACC + 2 * SSLOTS + 4;
@@ -394,6 +395,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   // Nothing above touches global memory, so the launch may overlap any kernel.  What that
   // kernel may have written is read below through L2, not through the read-only path.
   griddep_wait();
+  // A call of at most 32 rows fetches their indexes with the offsets (one latency, not two).
+  int* near_rows = reinterpret_cast<int*>(smem + Cfg::OFF_ROWS);
+  if constexpr (Cfg::SPLIT) {
+    const int i = static_cast<int>(threadIdx.x) - (Cfg::THREADS - BT);
+    if (g.rows && i >= 0 && i < g.T) near_rows[i] = __ldcg(g.rows + i);
+  }
+  auto row_index = [&](int t) {
+    if constexpr (Cfg::SPLIT) return near_rows[t];
+    else return __ldcg(g.rows + t);
+  };
   // offsets, held inside [0, T] and non-decreasing whatever the caller wrote
   for (int e = threadIdx.x; e <= g.E; e += Cfg::THREADS) lo[e] = min(max(__ldcg(g.offsets + e), 0), g.T);
   __syncthreads();
@@ -572,7 +583,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           // rows past the tile or outside the tokens are fetched as zeros
           auto token = [&](int i) {
             if (first + i >= tile.nrows) return g.M;
-            const int r = __ldcg(g.rows + tile.row0 + first + i);
+            const int r = row_index(tile.row0 + first + i);
             return static_cast<unsigned>(r) < static_cast<unsigned>(g.M) ? r : g.M;
           };
           const bool mine = j < half;
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const int c = i * 32 + lane;
           tok[i] = -1;
           if (c < tile.nrows) {
-            const int r = g.rows ? __ldcg(g.rows + tile.row0 + c) : tile.row0 + c;
+            const int r = g.rows ? row_index(tile.row0 + c) : tile.row0 + c;
             if (static_cast<unsigned>(r) < static_cast<unsigned>(g.M)) tok[i] = r;
           }
         }
