@@ -286,7 +286,7 @@ sq_status w8a8_grouped_mm(const int8_t* q_a, const float* s_tok, const int32_t* 
                           void* stream);
 
 /* FP8 block-scaled products grouped by expert: rows and offsets as above, the
- * arithmetic of fp8_block_mm (a call of at most 32 rows may sum K in 2 or 4
+ * arithmetic of fp8_block_mm (a call of at most 32 rows may sum K in 2 to 4
  * contiguous parts, each in order, and add the parts in order: the same from run
  * to run, but a row's last bits may differ from those of a larger call).  q_a
  * E4M3 [M,K], s_a fp32 [M, K/128], q_w E4M3 [E,N,K], s_w fp32 [E, N/128, K/128]

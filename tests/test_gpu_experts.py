@@ -262,6 +262,20 @@ def test_grouped_fp8(counts, N, K, gather):
     sq.check_device_error()
 
 
+@pytest.mark.parametrize("K", [768, 1152, 2048, 3200, 4224, 5120])
+@pytest.mark.parametrize("counts", [[0, 2, 0], [1, 1], [2]])
+def test_grouped_few_rows_over_uneven_parts(counts, K):
+    """Between 9 and 20 tiles, whose K is shared by two, three or four pairs, evenly or not."""
+    for N in (1152, 2304, 2432):
+        c = i8_case(counts, N - 16, K, True, 61 + K)
+        y = sq.w8a8_grouped_mm(*cuda(*c[:5]), rows=cuda(c[5])[0])
+        assert_bits(y, i8_reference(*c, torch.zeros(sum(counts), N - 16, dtype=torch.bfloat16)), "y")
+        c = fp8_case(counts, N, K, True, 62 + K)
+        y = sq.fp8_block_grouped_mm(*cuda(*c[:5]), rows=cuda(c[5])[0])
+        check_fp8(y, c, (N, K))
+    sq.check_device_error()
+
+
 @pytest.mark.parametrize("kind", ["i8", "fp8"])
 def test_grouped_answers_do_not_depend_on_timing(kind):
     """The same call many times, alone and under load on another stream: the same bits."""

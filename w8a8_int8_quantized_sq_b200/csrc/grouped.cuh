@@ -66,7 +66,7 @@ struct GroupedArgs {
   int T, M, E, N;
   int kb_total;            // K / 128
   int tiles_n;             // ceil(N / 256)
-  int split;               // CTA pairs that share a tile's K: 2 or 4 with tiles of 32 tokens, else 1
+  int split;               // CTA pairs that share a tile's K: 2 to 4 with tiles of 32 tokens, else 1
 };
 
 // Tensor maps of the token rows: boxes of 16, 32, 64 and 128 rows, of which a tile
@@ -81,16 +81,16 @@ struct GroupedMaps {
 // BT: most tokens per tile.  256 (INT8, two accumulators for a tile each) and 128 (FP8,
 // four for a K block each) fill the tensor memory.  32 is for calls of at most 32 rows
 // with so few tiles that most SMs would idle (an SM pair reads about 100 bytes/ns, and
-// a deeper ring does not change that): there a tile's K is split over the 2 or 4 CTA
+// a deeper ring does not change that): there a tile's K is split over the 2 to 4 CTA
 // pairs of one cluster.  The other pairs' partial sums meet in the first's shared
 // memory and are added in the order of K, so the answer does not depend on timing.
-// Measured with N = 2048, split and on one pair, us:
-//   1 row (8 tiles, 4 pairs, 2, 1),   K = 2048: INT8 8.0, 8.1, 9.0; FP8 8.9, 8.9, 9.9
-//                                     K = 5120: INT8 9.5, 11.3, 15.3; FP8 10.7, 12.6, 17.5
-//   2 rows in 2 experts (16 tiles),   K = 2048: INT8 8.3, 9.0; FP8 9.2, 10.0
-//                                     K = 5120: INT8 11.4, 15.2; FP8 12.8, 17.5
-//   4 rows in 4 experts (32 tiles),   K = 2048: INT8 9.2, 9.1; FP8 10.3, 10.2
-//                                     K = 5120: INT8 13.6, 16.0; FP8 15.0, 18.3
+// Measured with N = 2048, us, on the pairs given:
+//   1 row, 8 tiles, on 4, 2 and 1:   K = 2048: INT8 8.1, 8.2, 8.9; FP8 8.6, 8.6, 9.6
+//                                    K = 5120: INT8 9.4, 11.1, 14.7; FP8 10.1, 11.8, 15.6
+//   2 rows, 16 tiles, on 3, 2 and 1: K = 2048: INT8 8.2, 8.3, 8.9; FP8 9.0, 8.8, 9.7
+//                                    K = 5120: INT8 10.1, 11.2, 14.8; FP8 11.1, 11.9, 15.7
+//   4 rows, 32 tiles, on 2 and 1:    K = 2048: INT8 9.1, 9.0; FP8 10.0, 9.7
+//                                    K = 5120: INT8 13.6, 15.4; FP8 14.4, 16.3
 // With more tiles than resident clusters the 32-token tiles on one pair are no faster
 // than the wide ones (8 to 64 rows: 0 to 4 % slower), so those run the wide ones.
 template <bool F8_, int BT_>

@@ -805,10 +805,10 @@ sq_status silu_mul_quant(const void* gate_up, const float* inv_smooth, int fmt, 
 // 0 if it cannot be told.
 template <class Cfg>
 int grouped_clusters(int split) {
-  static std::atomic<int> cap[64][3];
+  static std::atomic<int> cap[64][4];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::atomic<int>& slot = cap[dev][split / 2];
+  std::atomic<int>& slot = cap[dev][split - 1];
   int mc = slot.load(std::memory_order_acquire);
   if (mc > 0) return mc;
   const int smem = Cfg::smem_bytes();
@@ -860,16 +860,17 @@ sq_status launch_grouped(const void* q_a, const void* q_w, const GroupedArgs& g,
                           Cfg::THREADS, Cfg::smem_bytes(), st, 2 * g.split, tw, tx, g);
 }
 
-// A tile's K over 4 or 2 pairs where every tile can have a resident cluster of its own
-// and a pair keeps two K blocks or more; else one pair per tile.  (Both measured, with
+// A tile's K over 4, 3 or 2 pairs where every tile can have a resident cluster of its own
+// and a pair keeps eight K blocks (of two pairs: two) or more, with fewer of which a larger
+// cluster gains nothing; else one pair per tile.  (Both measured, with
 // 32-token tiles on one pair too, beside the kernel.)
 template <bool F8>
 sq_status launch_grouped(const void* q_a, const void* q_w, GroupedArgs g, cudaStream_t st) {
   using Narrow = GroupedCfg<F8, 32>;
   using Wide = GroupedCfg<F8, F8 ? 128 : 256>;
   if (g.T <= Narrow::BT) {
-    for (g.split = 4; g.split > 1; g.split /= 2) {
-      if (g.kb_total < 2 * g.split) continue;
+    for (g.split = 4; g.split > 1; --g.split) {
+      if (g.kb_total < (g.split > 2 ? 8 : 2) * g.split) continue;
       const int mc = grouped_clusters<Narrow>(g.split);
       if (mc <= 0) return SQ_ERR_CUDA;
       if (grouped_tiles<Narrow>(g) <= mc) return launch_grouped<Narrow>(q_a, q_w, g, mc, st);
