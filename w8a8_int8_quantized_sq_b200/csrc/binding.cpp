@@ -209,8 +209,8 @@ PyObject* silu_mul_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
       inv = static_cast<float*>(t.data_ptr());
     }
     const bool per_row = !fp8 && group != 128;
-    auto t = make_all<2>({Out{{T, K}, 2, fp8 ? at::kByte : at::kChar}, Out{{T, K / 128}, per_row ? 1 : 2, at::kFloat}},
-                         dev);
+    const Out oq{{T, K}, 2, fp8 ? at::kByte : at::kChar}, os{{T, K / 128}, per_row ? 1 : 2, at::kFloat};
+    auto t = make_all<2>({oq, os}, dev);
     at::Tensor q = std::move(t[0]), sc = std::move(t[1]);
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     const sq_status rc = fp8 ? sq_silu_mul_quant_fp8(gu.data_ptr(), inv, static_cast<uint8_t*>(q.data_ptr()),
