@@ -139,7 +139,8 @@ struct GroupedCfg {
 // mbarrier wait without a suspend-time hint, bounded like wait_bounded, the same answer
 // in every lane: for the accumulators' round trip (MMA, commit, epilogue, release,
 // MMA), where waking from the hint's suspension showed (8198 rows, FP8 122 us against
-// 120; 32768 rows, INT8 123 against 121.5).  The other roles keep the hint: their polling would take issue slots.
+// 120; 32768 rows, INT8 123 against 121.5).  The other roles keep the hint: their
+// polling would take issue slots.
 __device__ __forceinline__ bool prompt_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

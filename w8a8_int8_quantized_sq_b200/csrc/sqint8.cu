@@ -813,8 +813,10 @@ int grouped_clusters(int split) {
   if (mc > 0) return mc;
   const int smem = Cfg::smem_bytes();
   if (cudaFuncSetAttribute(grouped_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
+      cudaSuccess) {
+    cudaGetLastError();
     return 0;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * split);
   cfg.blockDim = dim3(Cfg::THREADS);
@@ -826,7 +828,10 @@ int grouped_clusters(int split) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&mc, grouped_kernel<Cfg>, &cfg) != cudaSuccess || mc <= 0) return 0;
+  if (cudaOccupancyMaxActiveClusters(&mc, grouped_kernel<Cfg>, &cfg) != cudaSuccess || mc <= 0) {
+    cudaGetLastError();
+    return 0;
+  }
   slot.store(mc, std::memory_order_release);
   return mc;
 }
@@ -871,8 +876,7 @@ sq_status launch_grouped(const void* q_a, const void* q_w, GroupedArgs g, cudaSt
   if (g.T <= Narrow::BT) {
     for (g.split = 4; g.split > 1; --g.split) {
       if (g.kb_total < (g.split > 2 ? 8 : 2) * g.split) continue;
-      const int mc = grouped_clusters<Narrow>(g.split);
-      if (mc <= 0) return SQ_ERR_CUDA;
+      const int mc = grouped_clusters<Narrow>(g.split);  // 0 where no cluster of this size fits
       if (grouped_tiles<Narrow>(g) <= mc) return launch_grouped<Narrow>(q_a, q_w, g, mc, st);
     }
   }
