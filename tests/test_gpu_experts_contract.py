@@ -1,0 +1,51 @@
+"""What a caller of the mixture-of-experts operators may rely on beside their values."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import w8a8_int8_quantized_sq_b200 as sq
+from tests.test_gpu_experts import (assert_bits, call_norm, call_silu, check_fp8, check_silu, cuda,
+                                    i8_reference, layer_inputs, norm_reference, run_layer)
+
+pytestmark = pytest.mark.gpu
+
+
+def test_layer_run_repeats_itself():
+    """The same FP8 run many times, alone and under load on another stream: the same bits."""
+    a = layer_inputs(333, 8, 4, 1024, 512, "fp8", 208)
+    args = cuda(*a[:5], *a[5]["up"], *a[5]["down"])
+    want = run_layer(*args, "fp8")
+    load = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(40):
+            load @ load
+    got = [run_layer(*args, "fp8") for _ in range(60)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for g in got for x, y in zip(g, want))
+
+
+@pytest.mark.parametrize("fmt", ["i8", "fp8"])
+@pytest.mark.parametrize("M,E,top,K,I", [(1, 8, 2, 256, 128), (50, 16, 4, 512, 384)])
+def test_layer_run_step_by_step(M, E, top, K, I, fmt):
+    """Each operator of a run against its definition on what the one before it gave."""
+    h, res, gamma, rows, off, w, _, _ = layer_inputs(M, E, top, K, I, fmt, 209 + M)
+    d = cuda(h, res, gamma, rows, off, *w["up"], *w["down"])
+    mm = sq.w8a8_grouped_mm if fmt == "i8" else sq.fp8_block_grouped_mm
+    kept, q, s, r = call_norm(*d[:3], fmt)
+    k_ref, q_ref, s_ref = norm_reference(h, res, gamma, r.cpu(), fmt)
+    assert torch.equal(kept.cpu(), k_ref) and torch.equal(q.cpu(), q_ref) and torch.equal(s.cpu(), s_ref)
+    gu = mm(q, s, d[5], d[6], d[4], rows=d[3])
+    q2, s2 = call_silu(gu, None, fmt)
+    check_silu(gu.cpu(), None, fmt, q2, s2)
+    y = mm(q2, s2, d[7], d[8], d[4])
+    if fmt == "fp8":
+        check_fp8(gu, (q.cpu(), s.cpu(), *w["up"], off, rows), "up")
+        check_fp8(y, (q2.cpu(), s2.cpu(), *w["down"], off, None), "down")
+    else:
+        empty = torch.zeros(M * top, 2 * I, dtype=torch.bfloat16)
+        assert_bits(gu, i8_reference(q.cpu(), s.cpu(), *w["up"], off, rows, empty), "up")
+        empty = torch.zeros(M * top, K, dtype=torch.bfloat16)
+        assert_bits(y, i8_reference(q2.cpu(), s2.cpu(), *w["down"], off, None, empty), "down")
