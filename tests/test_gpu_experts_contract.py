@@ -5,8 +5,8 @@ import pytest
 import torch
 
 import w8a8_int8_quantized_sq_b200 as sq
-from tests.test_gpu_experts import (assert_bits, call_norm, call_silu, check_fp8, check_silu, cuda,
-                                    i8_reference, layer_inputs, norm_reference, run_layer)
+from tests.test_gpu_experts import (EPS, assert_bits, call_norm, call_silu, check_fp8, check_silu, cuda,
+                                    gen, i8_reference, layer_inputs, norm_reference, run_layer)
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,36 @@ def test_layer_run_step_by_step(M, E, top, K, I, fmt):
         assert_bits(gu, i8_reference(q.cpu(), s.cpu(), *w["up"], off, rows, empty), "up")
         empty = torch.zeros(M * top, K, dtype=torch.bfloat16)
         assert_bits(y, i8_reference(q2.cpu(), s2.cpu(), *w["down"], off, None, empty), "down")
+
+
+@pytest.mark.parametrize("between", ["norm", "activation"])
+def test_a_product_under_overlap_sees_weights_written_two_kernels_before(between):
+    """sq_set_overlap lets a product read its weights before the kernel directly ahead of it is
+    over, if that kernel does not write them.  A norm or an activation does not, and the
+    kernel that it follows is over when the product starts."""
+    N, K = 5120, 5120
+    w = [(torch.randn(N, K, generator=gen(210 + i)) * 0.02).bfloat16().cuda() for i in range(2)]
+    x = torch.randn(8, K, generator=gen(212)).bfloat16().cuda()
+    small = torch.randn(8, 512, generator=gen(213)).bfloat16().cuda()
+    gamma = torch.ones(512, device="cuda")
+    q_a, s_tok = sq.quant_per_token(x)
+    want = [sq.w8a8_scaled_mm(q_a, s_tok, *sq.quant_weight(v, None)) for v in w]
+    assert not torch.equal(*want)
+    q_w, s_ch = sq.quant_weight(w[1], None)
+    torch.cuda.synchronize()
+    write = sq.lib().sq_quant_weight
+    sq.set_overlap(True)
+    try:
+        for i in range(40):
+            rc = write(w[i % 2].data_ptr(), None, q_w.data_ptr(), s_ch.data_ptr(), N, K, 0,
+                       torch.cuda.current_stream().cuda_stream)
+            assert rc == 0
+            if between == "norm":
+                sq.add_rmsnorm_quant(small, small, gamma, EPS)
+            else:
+                sq.silu_mul_quant(small)
+            y = sq.w8a8_scaled_mm(q_a, s_tok, q_w, s_ch)
+            assert torch.equal(y, want[i % 2]), i
+    finally:
+        sq.set_overlap(False)
+    sq.check_device_error()

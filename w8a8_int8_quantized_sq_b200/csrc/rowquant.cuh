@@ -80,8 +80,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
   const int lane = threadIdx.x & 31;
   const int wig = t >> 5;
   const int K = p.K;
-  griddep_launch_dependents();
   griddep_wait();  // nothing above touches global memory: the launch may overlap any kernel
+  // The next kernel may start from here on, not before the wait: a product under
+  // sq_set_overlap reads its weights as soon as it starts, and only the kernel directly
+  // before it is known not to write them; the one before that has to be over.
+  griddep_launch_dependents();
 
   // The next row is requested as soon as this one is unpacked, so its loads are in
   // flight during the arithmetic (in the registers that this row's just left).
