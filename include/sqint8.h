@@ -235,8 +235,10 @@ sq_status fp8_block_mm(const uint8_t* q_a, const float* s_a, const uint8_t* q_w,
  * fp32 (amax below about 3.7e-37).
  * h, residual, residual_out BF16 [M,K]; residual_out may be the residual or h
  * itself (in place); one that overlaps them otherwise is refused (SQ_ERR_SHAPE).
- * inv_rms (fp32 [M], may be NULL) receives r.  eps > 0; K <= 24576.  A row that
- * holds inf or NaN has unspecified codes and scales; the other rows are not
+ * inv_rms (fp32 [M], may be NULL) receives r.  eps > 0; K <= 24576.  Where a row
+ * (group == 128: 128 columns of it) has a v that is NaN or infinite, its scale is
+ * NaN or infinite, so that products with it are too, and its codes are
+ * unspecified; a NaN in x is in every v of its row.  The other rows are not
  * affected.  The launch may overlap the tail of any preceding kernel (it reads
  * and writes nothing before that kernel's end). */
 sq_status sq_add_rmsnorm_quant(const void* h_bf16, const void* residual_bf16, const float* gamma,

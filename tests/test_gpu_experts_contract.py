@@ -6,7 +6,7 @@ import torch
 
 import w8a8_int8_quantized_sq_b200 as sq
 from tests.test_gpu_experts import (EPS, assert_bits, call_norm, call_silu, check_fp8, check_silu, cuda,
-                                    gen, i8_reference, layer_inputs, norm_reference, run_layer)
+                                    gen, i8_reference, layer_inputs, norm_case, norm_reference, run_layer)
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,74 @@ def test_a_product_under_overlap_sees_weights_written_two_kernels_before(between
     finally:
         sq.set_overlap(False)
     sq.check_device_error()
+
+
+def products(q, sc, fmt):
+    """The codes and scales through a grouped product of one expert (weights of ones)."""
+    T, K = q.shape
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    if fmt == "fp8":
+        w = torch.full((1, 128, K), 0x38, dtype=torch.uint8, device="cuda")
+        return sq.fp8_block_grouped_mm(q, sc, w, torch.ones(1, 1, K // 128, device="cuda"), off)
+    w = torch.ones(1, 128, K, dtype=torch.int8, device="cuda")
+    return sq.w8a8_grouped_mm(q, sc, w, torch.ones(1, 128, device="cuda"), off)
+
+
+@pytest.mark.parametrize("fmt", ["i8", "i8_group", "fp8"])
+@pytest.mark.parametrize("K", [256, 1152, 2048, 5120, 17408])
+def test_norm_of_a_nonfinite_row_has_a_nonfinite_scale(K, fmt):
+    h, res, gamma = norm_case(9, K, 201)
+    clean = [t.cpu() for t in call_norm(*cuda(h, res, gamma), fmt)]
+    h[1, 7], res[3, K - 9], h[5, 0], res[7, K // 2] = float("nan"), float("inf"), -float("inf"), float("nan")
+    got = call_norm(*cuda(h, res, gamma), fmt)
+    sc = got[2].cpu().view(9, -1)
+    at = {1: slice(None), 7: slice(None)}           # a NaN is in every value of its row
+    at |= {3: -1, 5: 0}                             # 1 / rms is 0: zeros beside the infinity's NaN
+    for row, where in at.items():
+        assert not torch.isfinite(sc[row][where]).any(), (row, sc[row])
+    for a, b in zip(got, clean):
+        assert torch.equal(a.cpu()[[0, 2, 4, 6, 8]], b[[0, 2, 4, 6, 8]])
+    if fmt != "i8_group":
+        bad = torch.isfinite(products(got[1], got[2], fmt).cpu()).sum(1)
+        assert bad.tolist() == [128, 0] * 4 + [128]
+
+
+@pytest.mark.parametrize("fmt", ["i8", "i8_group", "fp8"])
+@pytest.mark.parametrize("K", [256, 768, 1408, 5120, 17408])
+def test_activation_of_a_nonfinite_row_has_a_nonfinite_scale(K, fmt):
+    gu = (torch.randn(9, 2 * K, generator=gen(202)) * 2).bfloat16()
+    gu[:, [3, K - 100]] = 2.0
+    gu[:, [K + 3, 2 * K - 100]] = 1.5
+    clean = [t.cpu() for t in call_silu(gu.cuda(), None, fmt)]
+    gu[1, 3], gu[2, K + 3] = float("nan"), float("nan")
+    gu[3, 3], gu[4, K + 3] = float("inf"), -float("inf")   # silu(inf) = inf
+    gu[5, K - 100], gu[6, 3] = -float("inf"), 3e38
+    gu[6, K + 3] = 3e38                                    # a product past the range
+    got = call_silu(gu.cuda(), None, fmt)
+    sc, ref = got[1].cpu().view(9, -1), clean[1].view(9, -1)
+    bad = {1: 0, 2: 0, 3: 0, 4: 0, 5: (K - 100) // 128 if fmt != "i8" else 0, 6: 0}
+    for row, g in bad.items():
+        assert not torch.isfinite(sc[row, g]), row
+        keep = torch.ones(sc.shape[1], dtype=torch.bool)
+        keep[g] = False
+        assert torch.equal(sc[row][keep], ref[row][keep])
+    for row in (1, 2):
+        assert torch.isnan(sc[row, 0])
+    for row in (3, 4, 6):
+        assert sc[row, 0] == float("inf")
+    for a, b in zip(got, clean):
+        assert torch.equal(a.cpu()[[0, 7, 8]], b[[0, 7, 8]])
+    if fmt != "i8_group":
+        ok = torch.isfinite(products(got[0], got[1], fmt).cpu()).sum(1)
+        assert ok.tolist() == [128] + [0] * 6 + [128] * 2
+
+
+def test_activation_of_an_infinite_gate():
+    """silu(inf) u = inf u, and the largest finite gates are not touched by what guards it."""
+    K = 128
+    gu = torch.ones(4, 2 * K)
+    gu[0, :K], gu[1, :K], gu[2, :K], gu[3, :K] = float("inf"), 3e38, 2.0 ** 17, 2.0 ** 18
+    gu = gu.bfloat16()
+    q, sc = call_silu(gu.cuda(), None, "i8")
+    assert sc[0] == float("inf")
+    check_silu(gu[1:], None, "i8", q[1:], sc[1:])

@@ -12,9 +12,9 @@
 // 5 (activation).  Measured:
 //   norm, INT8 per token, 8192 x 5120: 47.9 us, 6130 GB/s; one row per block and no
 //     prefetch 52.9 us; 512 threads per row 69 us.
-//   activation, E4M3, 32768 x 1024: 28.5 us, 5890 GB/s (64 threads x 2 vectors);
-//     32 x 4 31.0 us, 128 x 1 29.9 us; with __expf and __fdividef 31.1 us; one row
-//     per warp, none ahead, 47 us.
+//   activation, E4M3, 32768 x 1024: 29.4 us, 5710 GB/s (64 threads x 2 vectors).  Without
+//     the guard of an infinite gate 28.7 us, and against that: 32 x 4 31.0 us, 128 x 1
+//     29.9 us; with __expf and __fdividef 31.1 us; one row per warp, none ahead, 47 us.
 #pragma once
 #include "quant.cuh"
 
@@ -42,16 +42,27 @@ struct RowQuantArgs {
 // 2^(-g log2 e) = 2^(-g H) (1 - g L ln 2 + ...), where the next term is below 2^-23 for g
 // >= -87.  With the roundings of the product, the sum and the last two products (2^-24
 // each) the result is within 2^-20 of its value for g >= -87; below, the value and its
-// error are less than 2^-110 |u|.  L > 0 keeps an overflowed exponential infinite.
-// (g log2(e) rounded to fp32 took the same time: 28.2 and 28.3 us, E4M3 32768 x 1024;
+// error are less than 2^-110 |u|.  L > 0 keeps an overflowed exponential infinite, and
+// -g L ln 2 is held at -1, where the exponential has long been zero (g > 2^17), so that
+// an infinite g does not make it 0 * inf: silu(inf) = inf.  (That guard costs 0.6 us of
+// 29.4, E4M3 32768 x 1024; the arithmetic on pairs of values, with it, took the same.)
+// (Without it: g log2(e) rounded to fp32 took the same time: 28.2 and 28.3 us, E4M3 32768 x 1024;
 // a division in place of the reciprocal and expf 44 us.  Codes on the other side of a
 // rounding border than in 64 bits, of 33.5 M: 25 to 33; with the division and expf 27 to 32.)
 __device__ __forceinline__ float silu_mul(float g, float u) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.44268798828125f)));
-  e = __fmaf_rn(e, __fmul_rn(g, -4.888495152e-06f), e);
+  e = __fmaf_rn(e, fmaxf(__fmul_rn(g, -4.888495152e-06f), -1.0f), e);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
   return __fmul_rn(__fmul_rn(g, r), u);
+}
+
+// The larger, NaN if either is (fmaxf would drop it): a row that holds NaN has scale NaN, so
+// what is computed from it is NaN, not a plausible number.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
 }
 
 // Codes per value: f32(QMAX * f32(1 / amax)), held finite (a largest magnitude
@@ -190,22 +201,22 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     for (int j = 0; j < NV; ++j) {
       float m = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
+      for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(v[j][i]));
       if constexpr (GROUP) {
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        for (int off = 8; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
       }
       gmax[j] = m;
-      amax = fmaxf(amax, m);
+      amax = max_nan(amax, m);
     }
     if constexpr (!GROUP) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
       if constexpr (NW > 1) {
         if (lane == 0) red[slot][rib][wig] = amax;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < NW; ++w) amax = fmaxf(amax, red[slot][rib][w]);
+        for (int w = 0; w < NW; ++w) amax = max_nan(amax, red[slot][rib][w]);
       }
       if (active && t == 0) p.scales[row] = __fmul_rn(amax, 1.0f / QMAX);
     }
