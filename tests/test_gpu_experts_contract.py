@@ -1,6 +1,8 @@
 """What a caller of the mixture-of-experts operators may rely on beside their values."""
 from __future__ import annotations
 
+import io
+
 import pytest
 import torch
 
@@ -153,3 +155,25 @@ def test_activation_of_an_infinite_gate():
     q, sc = call_silu(gu.cuda(), None, "i8")
     assert sc[0] == float("inf")
     check_silu(gu[1:], None, "i8", q[1:], sc[1:])
+
+
+@pytest.mark.parametrize("M", [1, 3, 2000])
+@pytest.mark.parametrize("fmt", ["i8", "i8_group", "fp8"])
+def test_outputs_of_one_call_have_storages_of_their_own(fmt, M):
+    """Growing one output, freeing its memory or saving it touches no other."""
+    h = torch.randn(M, 768, generator=gen(203)).bfloat16().cuda()
+    gamma = torch.rand(768, device="cuda") + 0.25
+    for call in (lambda: call_norm(h, h, gamma, fmt), lambda: call_silu(h, None, fmt),
+                 lambda: call_norm(h, h, gamma, fmt, residual_out=h.clone())):
+        want = [t.clone() for t in call()]
+        for i in range(len(want)):
+            outs = call()
+            assert outs[i].untyped_storage().nbytes() == want[i].numel() * want[i].element_size()
+            outs[i].resize_(outs[i].numel() + 70000).fill_(1)
+            assert all(torch.equal(a, b) for j, (a, b) in enumerate(zip(outs, want)) if j != i)
+            outs = call()
+            outs[i].untyped_storage().resize_(0)
+            assert all(torch.equal(a, b) for j, (a, b) in enumerate(zip(outs, want)) if j != i)
+            file = io.BytesIO()
+            torch.save(call()[i], file)
+            assert file.tell() < want[i].numel() * want[i].element_size() + 4096

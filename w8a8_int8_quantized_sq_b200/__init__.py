@@ -358,7 +358,6 @@ def fp8_block_mm(q_a, s_a, q_w, s_w):
 # extension _binding.so (csrc/binding.cpp).  Tensors may be on any CUDA device: the
 # launch goes to theirs, on that device's current stream.  A tensor of another type,
 # shape, layout or device raises ValueError; what the library refuses raises SqError.
-# Outputs of one call that take at most 1 MiB together are parts of one allocation.
 
 _ext = None
 

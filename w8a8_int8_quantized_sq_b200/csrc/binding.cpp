@@ -15,7 +15,6 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <array>
 #include <stdexcept>
 #include <string>
 
@@ -60,49 +59,16 @@ int device_of(const char* fn, const char* name, const at::Tensor& t, int64_t dim
   return t.get_device();
 }
 
-// Straight from the caching allocator: at::empty's dispatch costs as much again.
+// Straight from the caching allocator: at::empty's dispatch costs as much again.  Every output
+// has a storage of its own, as a torch caller expects: resizing, freeing or saving one touches
+// no other.  (Parts of one allocation took 0.5 us less for each further output.)
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)),
                                 std::nullopt);
 }
 
-struct Out {
-  std::array<int64_t, 2> shape;
-  int dims;
-  at::ScalarType type;
-  at::IntArrayRef sizes() const { return {shape.data(), static_cast<size_t>(dims)}; }
-  size_t bytes() const {
-    size_t n = c10::elementSize(type);
-    for (int i = 0; i < dims; ++i) n *= static_cast<size_t>(shape[i]);
-    return n;
-  }
-};
-
-// The outputs of one call.  Together at most 1 MiB (a call of a few tokens, whose host time
-// counts: an allocation takes 0.5 us) they are parts of one allocation, 256 bytes
-// aligned; larger ones each have their own, so that keeping one does not keep the
-// others' memory.  Norm of 8 tokens: 5.7 us a call with four allocations, 4.3 with one.
-template <size_t N>
-std::array<at::Tensor, N> make_all(const std::array<Out, N>& outs, int dev) {
-  std::array<at::Tensor, N> t;
-  size_t total = 0;
-  for (const Out& o : outs) total += (o.bytes() + 255) & ~size_t{255};
-  if (total > (size_t{1} << 20)) {
-    for (size_t i = 0; i < N; ++i) t[i] = make(outs[i].sizes(), outs[i].type, dev);
-    return t;
-  }
-  const at::Tensor all = make({static_cast<int64_t>(total)}, at::kByte, dev);
-  size_t at = 0;
-  for (size_t i = 0; i < N; ++i) {
-    t[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()),
-                                                    c10::DispatchKeySet(c10::DispatchKey::CUDA),
-                                                    c10::scalarTypeToTypeMeta(outs[i].type));
-    c10::TensorImpl* impl = t[i].unsafeGetTensorImpl();
-    impl->set_storage_offset(static_cast<int64_t>(at / c10::elementSize(outs[i].type)));
-    impl->set_sizes_contiguous(outs[i].sizes());
-    at += (outs[i].bytes() + 255) & ~size_t{255};
-  }
-  return t;
+at::Tensor make_scales(int64_t rows, int64_t K, bool per_row, int dev) {
+  return per_row ? make({rows}, at::kFloat, dev) : make({rows, K / 128}, at::kFloat, dev);
 }
 
 PyObject* fail(const char* fn, sq_status rc) {
@@ -154,19 +120,15 @@ PyObject* add_rmsnorm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fits(fn, "h", h, dev, at::kBFloat16, {M, K});
     fits(fn, "residual", res, dev, at::kBFloat16, {M, K});
     fits(fn, "gamma", gamma, dev, at::kFloat, {K});
-    const bool per_row = !fp8 && group != 128;
-    const Out oq{{M, K}, 2, fp8 ? at::kByte : at::kChar}, os{{M, K / 128}, per_row ? 1 : 2, at::kFloat},
-        orr{{M}, 1, at::kFloat};
-    at::Tensor out, q, sc, r;
+    at::Tensor out;
     if (a[5] == Py_None) {
-      auto t = make_all<4>({Out{{M, K}, 2, at::kBFloat16}, oq, os, orr}, dev);
-      out = std::move(t[0]), q = std::move(t[1]), sc = std::move(t[2]), r = std::move(t[3]);
+      out = make({M, K}, at::kBFloat16, dev);
     } else {
       out = tensor(a[5], fn, "residual_out");
       fits(fn, "residual_out", out, dev, at::kBFloat16, {M, K});
-      auto t = make_all<3>({oq, os, orr}, dev);
-      q = std::move(t[0]), sc = std::move(t[1]), r = std::move(t[2]);
     }
+    at::Tensor q = make({M, K}, fp8 ? at::kByte : at::kChar, dev), sc = make_scales(M, K, !fp8 && group != 128, dev),
+               r = make({M}, at::kFloat, dev);
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     const sq_status rc =
         fp8 ? sq_add_rmsnorm_quant_fp8(h.data_ptr(), res.data_ptr(), static_cast<float*>(gamma.data_ptr()),
@@ -208,10 +170,7 @@ PyObject* silu_mul_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
       fits(fn, "inv_s", t, dev, at::kFloat, {K});
       inv = static_cast<float*>(t.data_ptr());
     }
-    const bool per_row = !fp8 && group != 128;
-    const Out oq{{T, K}, 2, fp8 ? at::kByte : at::kChar}, os{{T, K / 128}, per_row ? 1 : 2, at::kFloat};
-    auto t = make_all<2>({oq, os}, dev);
-    at::Tensor q = std::move(t[0]), sc = std::move(t[1]);
+    at::Tensor q = make({T, K}, fp8 ? at::kByte : at::kChar, dev), sc = make_scales(T, K, !fp8 && group != 128, dev);
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     const sq_status rc = fp8 ? sq_silu_mul_quant_fp8(gu.data_ptr(), inv, static_cast<uint8_t*>(q.data_ptr()),
                                                      static_cast<float*>(sc.data_ptr()), T, K, stream_of(dev))
