@@ -2,13 +2,15 @@
 from __future__ import annotations
 
 import io
+import threading
+import time
 
 import pytest
 import torch
 
 import w8a8_int8_quantized_sq_b200 as sq
 from tests.test_gpu_experts import (EPS, assert_bits, call_norm, call_silu, check_fp8, check_silu, cuda,
-                                    gen, i8_reference, layer_inputs, norm_case, norm_reference, run_layer)
+                                    gen, i8_case, i8_reference, layer_inputs, norm_case, norm_reference, run_layer)
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +179,40 @@ def test_outputs_of_one_call_have_storages_of_their_own(fmt, M):
             file = io.BytesIO()
             torch.save(call()[i], file)
             assert file.tell() < want[i].numel() * want[i].element_size() + 4096
+
+
+def test_a_full_launch_queue_stops_no_other_host_thread():
+    """While a call waits for room in the launch queue (behind work that lasts a good second),
+    another thread goes on.  A thread that holds the interpreter's lock would stop it."""
+    x = torch.randn(4, 256, device="cuda").bfloat16()
+    q_a, s_a, q_w, s_w, off, _ = cuda(*i8_case([4], 128, 128, False, 204))
+    gamma = torch.ones(256, device="cuda")
+    for call in (lambda: sq.silu_mul_quant(x), lambda: sq.add_rmsnorm_quant(x, x, gamma, EPS),
+                 lambda: sq.w8a8_grouped_mm(q_a, s_a, q_w, s_w, off)):
+        call()
+        torch.cuda.synchronize()
+        gaps, stop = [], threading.Event()
+
+        def tick():
+            last = time.perf_counter()
+            while not stop.is_set():
+                time.sleep(0.001)
+                now = time.perf_counter()
+                gaps.append(now - last)
+                last = now
+
+        t = threading.Thread(target=tick)
+        t.start()
+        torch.cuda._sleep(2_000_000_000)
+        longest = 0.0
+        for _ in range(3000):
+            t0 = time.perf_counter()
+            call()
+            longest = max(longest, time.perf_counter() - t0)
+            if longest > 0.2:
+                break
+        stop.set()
+        t.join()
+        torch.cuda.synchronize()
+        assert longest > 0.2, "the launch queue never filled"
+        assert max(gaps) < longest / 2, (max(gaps), longest)

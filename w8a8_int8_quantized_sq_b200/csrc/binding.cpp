@@ -82,6 +82,14 @@ PyObject* fail(const char* fn, sq_status rc) {
 
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
+// Without the interpreter's lock while it lives, like torch's own calls: an allocation may wait
+// for the device and a launch for room in its queue, and other host threads have to
+// go on meanwhile (a host callback that the queue waits for may be one of theirs).
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 template <class F>
 PyObject* guarded(F&& f) {
   try {
@@ -120,25 +128,28 @@ PyObject* add_rmsnorm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fits(fn, "h", h, dev, at::kBFloat16, {M, K});
     fits(fn, "residual", res, dev, at::kBFloat16, {M, K});
     fits(fn, "gamma", gamma, dev, at::kFloat, {K});
-    at::Tensor out;
-    if (a[5] == Py_None) {
-      out = make({M, K}, at::kBFloat16, dev);
-    } else {
+    at::Tensor out, q, sc, r;
+    if (a[5] != Py_None) {
       out = tensor(a[5], fn, "residual_out");
       fits(fn, "residual_out", out, dev, at::kBFloat16, {M, K});
     }
-    at::Tensor q = make({M, K}, fp8 ? at::kByte : at::kChar, dev), sc = make_scales(M, K, !fp8 && group != 128, dev),
-               r = make({M}, at::kFloat, dev);
-    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
-    const sq_status rc =
-        fp8 ? sq_add_rmsnorm_quant_fp8(h.data_ptr(), res.data_ptr(), static_cast<float*>(gamma.data_ptr()),
-                                       static_cast<float>(eps), out.data_ptr(),
-                                       static_cast<uint8_t*>(q.data_ptr()), static_cast<float*>(sc.data_ptr()),
-                                       static_cast<float*>(r.data_ptr()), M, K, stream_of(dev))
-            : sq_add_rmsnorm_quant(h.data_ptr(), res.data_ptr(), static_cast<float*>(gamma.data_ptr()),
-                                   static_cast<float>(eps), group, out.data_ptr(),
-                                   static_cast<int8_t*>(q.data_ptr()), static_cast<float*>(sc.data_ptr()),
-                                   static_cast<float*>(r.data_ptr()), M, K, stream_of(dev));
+    sq_status rc;
+    {
+      Unlocked unlocked;
+      if (!out.defined()) out = make({M, K}, at::kBFloat16, dev);
+      q = make({M, K}, fp8 ? at::kByte : at::kChar, dev);
+      sc = make_scales(M, K, !fp8 && group != 128, dev);
+      r = make({M}, at::kFloat, dev);
+      c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+      rc = fp8 ? sq_add_rmsnorm_quant_fp8(h.data_ptr(), res.data_ptr(), static_cast<float*>(gamma.data_ptr()),
+                                          static_cast<float>(eps), out.data_ptr(),
+                                          static_cast<uint8_t*>(q.data_ptr()), static_cast<float*>(sc.data_ptr()),
+                                          static_cast<float*>(r.data_ptr()), M, K, stream_of(dev))
+               : sq_add_rmsnorm_quant(h.data_ptr(), res.data_ptr(), static_cast<float*>(gamma.data_ptr()),
+                                      static_cast<float>(eps), group, out.data_ptr(),
+                                      static_cast<int8_t*>(q.data_ptr()), static_cast<float*>(sc.data_ptr()),
+                                      static_cast<float*>(r.data_ptr()), M, K, stream_of(dev));
+    }
     if (rc != SQ_OK) return fail(fn, rc);
     PyObject* o = nullptr;
     if (a[5] == Py_None) {
@@ -170,12 +181,18 @@ PyObject* silu_mul_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
       fits(fn, "inv_s", t, dev, at::kFloat, {K});
       inv = static_cast<float*>(t.data_ptr());
     }
-    at::Tensor q = make({T, K}, fp8 ? at::kByte : at::kChar, dev), sc = make_scales(T, K, !fp8 && group != 128, dev);
-    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
-    const sq_status rc = fp8 ? sq_silu_mul_quant_fp8(gu.data_ptr(), inv, static_cast<uint8_t*>(q.data_ptr()),
-                                                     static_cast<float*>(sc.data_ptr()), T, K, stream_of(dev))
-                             : sq_silu_mul_quant(gu.data_ptr(), inv, group, static_cast<int8_t*>(q.data_ptr()),
-                                                 static_cast<float*>(sc.data_ptr()), T, K, stream_of(dev));
+    at::Tensor q, sc;
+    sq_status rc;
+    {
+      Unlocked unlocked;
+      q = make({T, K}, fp8 ? at::kByte : at::kChar, dev);
+      sc = make_scales(T, K, !fp8 && group != 128, dev);
+      c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+      rc = fp8 ? sq_silu_mul_quant_fp8(gu.data_ptr(), inv, static_cast<uint8_t*>(q.data_ptr()),
+                                       static_cast<float*>(sc.data_ptr()), T, K, stream_of(dev))
+               : sq_silu_mul_quant(gu.data_ptr(), inv, group, static_cast<int8_t*>(q.data_ptr()),
+                                   static_cast<float*>(sc.data_ptr()), T, K, stream_of(dev));
+    }
     if (rc != SQ_OK) return fail(fn, rc);
     return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(q)), THPVariable_Wrap(std::move(sc)));
   });
@@ -211,22 +228,24 @@ PyObject* grouped_mm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       rows = static_cast<const int32_t*>(r.data_ptr());
     }
     at::Tensor y;
-    if (a[6] == Py_None) {
-      y = make({T, N}, at::kBFloat16, dev);
-    } else {
+    if (a[6] != Py_None) {
       y = tensor(a[6], fn, "out");
       fits(fn, "out", y, dev, at::kBFloat16, {T, N});
     }
-    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     const float *psa = static_cast<const float*>(sa.data_ptr()), *psw = static_cast<const float*>(sw.data_ptr());
     const int32_t* poff = static_cast<const int32_t*>(off.data_ptr());
-    const sq_status rc =
-        fp8 ? fp8_block_grouped_mm(static_cast<const uint8_t*>(qa.data_ptr()), psa, rows,
-                                   static_cast<const uint8_t*>(qw.data_ptr()), psw, poff, y.data_ptr(), T, M,
-                                   E, N, K, stream_of(dev))
-            : w8a8_grouped_mm(static_cast<const int8_t*>(qa.data_ptr()), psa, rows,
-                              static_cast<const int8_t*>(qw.data_ptr()), psw, poff, y.data_ptr(), T, M, E, N,
-                              K, stream_of(dev));
+    sq_status rc;
+    {
+      Unlocked unlocked;
+      if (!y.defined()) y = make({T, N}, at::kBFloat16, dev);
+      c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+      rc = fp8 ? fp8_block_grouped_mm(static_cast<const uint8_t*>(qa.data_ptr()), psa, rows,
+                                      static_cast<const uint8_t*>(qw.data_ptr()), psw, poff, y.data_ptr(), T, M, E,
+                                      N, K, stream_of(dev))
+               : w8a8_grouped_mm(static_cast<const int8_t*>(qa.data_ptr()), psa, rows,
+                                 static_cast<const int8_t*>(qw.data_ptr()), psw, poff, y.data_ptr(), T, M, E, N, K,
+                                 stream_of(dev));
+    }
     if (rc != SQ_OK) return fail(fn, rc);
     if (a[6] != Py_None) {
       Py_INCREF(a[6]);
