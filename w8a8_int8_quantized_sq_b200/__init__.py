@@ -363,15 +363,19 @@ _ext = None
 
 
 def _extension():
-    """Load the extension; raises if it is missing."""
+    """Load the extension; raises if it is missing or was built for another PyTorch or Python."""
     global _ext
     if _ext is None:
         lib()
+        from . import build
+        how = "build it with `python -m w8a8_int8_quantized_sq_b200.build`"
         try:
             from . import _binding as ext
         except ImportError as e:
-            raise RuntimeError(f"{os.path.join(_HERE, '_binding.so')} cannot be loaded ({e}): build "
-                               "it with `python -m w8a8_int8_quantized_sq_b200.build`") from e
+            raise RuntimeError(f"{build.BINDING} cannot be loaded ({e}): {how}") from e
+        if ext.built_for != build.binding_key():
+            raise RuntimeError(f"{build.BINDING} is for \"{ext.built_for}\", this is "
+                               f"\"{build.binding_key()}\": {how}")
         ext.set_errors(SqError, torch.OutOfMemoryError)
         _ext = ext
     return _ext

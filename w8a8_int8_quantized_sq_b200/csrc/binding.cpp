@@ -276,4 +276,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&kModule);
+  // what this file was compiled for (build.py), compared when it is loaded
+  if (m && PyModule_AddStringConstant(m, "built_for", SQ_BINDING_KEY) != 0) Py_CLEAR(m);
+  return m;
+}
