@@ -64,6 +64,15 @@ def test_a_change_rebuilds_and_is_refused_until_then(built, monkeypatch, change)
     assert len(built) == 1  # once
 
 
+def test_a_file_that_does_not_say_is_refused(built, monkeypatch):
+    sq._extension()
+    monkeypatch.setattr(sq, "_ext", None)
+    from w8a8_int8_quantized_sq_b200 import _binding
+    monkeypatch.delattr(_binding, "built_for")
+    with pytest.raises(RuntimeError, match="unknown.*build it with"):
+        sq._extension()
+
+
 def test_a_missing_key_rebuilds(built):
     os.remove(sq_build.BINDING + ".key")
     sq_build.build_binding()

@@ -373,8 +373,9 @@ def _extension():
             from . import _binding as ext
         except ImportError as e:
             raise RuntimeError(f"{build.BINDING} cannot be loaded ({e}): {how}") from e
-        if ext.built_for != build.binding_key():
-            raise RuntimeError(f"{build.BINDING} is for \"{ext.built_for}\", this is "
+        built_for = getattr(ext, "built_for", "unknown")
+        if built_for != build.binding_key():
+            raise RuntimeError(f"{build.BINDING} is for \"{built_for}\", this is "
                                f"\"{build.binding_key()}\": {how}")
         ext.set_errors(SqError, torch.OutOfMemoryError)
         _ext = ext
