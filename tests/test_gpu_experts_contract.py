@@ -10,7 +10,8 @@ import torch
 
 import w8a8_int8_quantized_sq_b200 as sq
 from tests.test_gpu_experts import (EPS, assert_bits, call_norm, call_silu, check_fp8, check_silu, cuda,
-                                    gen, i8_case, i8_reference, layer_inputs, norm_case, norm_reference, run_layer)
+                                    fp8_case, gen, i8_case, i8_reference, layer_inputs, norm_case, norm_reference,
+                                    run_layer)
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +217,68 @@ def test_a_full_launch_queue_stops_no_other_host_thread():
         torch.cuda.synchronize()
         assert longest > 0.2, "the launch queue never filled"
         assert max(gaps) < longest / 2, (max(gaps), longest)
+
+
+def shifted(t, by=1):
+    """The same values in a view that starts `by` elements into its storage."""
+    flat = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+    view = flat[by:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("kind,K", [("i8", 256), ("fp8", 640), ("fp8", 512)])
+def test_grouped_operands_that_start_anywhere(kind, K):
+    """Scales, offsets and row indexes may be views at any element."""
+    counts = [5, 0, 40, 7, 300]
+    c = (i8_case if kind == "i8" else fp8_case)(counts, 256, K, True, 205)
+    mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+    q_a, s_a, q_w, s_w, off, rows = cuda(*c)
+    want = mm(q_a, s_a, q_w, s_w, off, rows=rows)
+    for by in (1, 2, 3):
+        assert shifted(off, by).data_ptr() % 16
+        assert torch.equal(mm(q_a, s_a, q_w, s_w, shifted(off, by), rows=rows), want)
+        assert torch.equal(mm(q_a, s_a, q_w, s_w, off, rows=shifted(rows, by)), want)
+        assert torch.equal(mm(q_a, shifted(s_a, by), q_w, s_w, off, rows=rows), want)
+        assert torch.equal(mm(q_a, s_a, q_w, shifted(s_w, by), off, rows=rows), want)
+        assert torch.equal(mm(q_a, shifted(s_a, by), q_w, shifted(s_w, by), shifted(off, by),
+                              rows=shifted(rows, by)), want)
+    sq.check_device_error()
+
+
+@pytest.mark.parametrize("kind", ["i8", "fp8"])
+def test_grouped_call_on_a_range_of_experts(kind):
+    """offsets[e0 : e1 + 1] with the range's weights: its rows as in the whole call, the others
+    left; eager and captured."""
+    counts = [5, 0, 40, 7, 3, 20, 0, 9]
+    c = (i8_case if kind == "i8" else fp8_case)(counts, 128, 384, True, 206)
+    mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+    q_a, s_a, q_w, s_w, off, rows = cuda(*c)
+    want = mm(q_a, s_a, q_w, s_w, off, rows=rows)
+    bounds = off.tolist()
+    out = torch.empty_like(want)
+    for e0 in range(len(counts)):
+        for e1 in range(e0 + 1, len(counts) + 1):
+            graph = torch.cuda.CUDAGraph()
+            call = lambda: mm(q_a, s_a, q_w[e0:e1], s_w[e0:e1], off[e0:e1 + 1], rows=rows, out=out)
+            with torch.cuda.graph(graph):
+                call()
+            for go in (call, graph.replay):
+                out.fill_(7.0)
+                go()
+                lo, hi = bounds[e0], bounds[e1]
+                assert torch.equal(out[lo:hi], want[lo:hi])
+                assert (out[:lo] == 7).all() and (out[hi:] == 7).all()
+    sq.check_device_error()
+
+
+@pytest.mark.parametrize("fmt", ["i8", "i8_group", "fp8"])
+def test_factors_that_start_anywhere(fmt):
+    """gamma and inv_s may be views at any element; a gradient that they ask for is not recorded."""
+    h, res, gamma = cuda(*norm_case(5, 768, 214))
+    want, act = call_norm(h, res, gamma, fmt), call_silu(h, gamma[:384].clone(), fmt)
+    for by in (1, 2, 3):
+        got = call_norm(h, res, shifted(gamma, by).requires_grad_(), fmt)
+        got += call_silu(h, shifted(gamma[:384], by).requires_grad_(), fmt)
+        assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, (*want, *act)))
+    sq.check_device_error()

@@ -358,6 +358,8 @@ def fp8_block_mm(q_a, s_a, q_w, s_w):
 # extension _binding.so (csrc/binding.cpp).  Tensors may be on any CUDA device: the
 # launch goes to theirs, on that device's current stream.  A tensor of another type,
 # shape, layout or device raises ValueError; what the library refuses raises SqError.
+# Scales, gamma, inv_s, offsets and rows may be views that start at any element (those
+# that do not start at 16 bytes are copied first); the matrices have to start at 16 bytes.
 
 _ext = None
 

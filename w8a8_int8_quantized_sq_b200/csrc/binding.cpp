@@ -71,6 +71,17 @@ at::Tensor make_scales(int64_t rows, int64_t K, bool per_row, int dev) {
   return per_row ? make({rows}, at::kFloat, dev) : make({rows, K / 128}, at::kFloat, dev);
 }
 
+// The C entry points want 16-byte aligned operands.  Scales, factors, offsets and row indexes may
+// be views that start at any element (a range of experts, a chunk of tokens): then they
+// are copied, in stream order, to memory of their own, which is `t` from then on.
+void align(at::Tensor& t) {
+  if (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0) return;
+  at::AutoDispatchBelowADInplaceOrView plain;  // no gradient is recorded
+  at::Tensor copy = make(t.sizes(), t.scalar_type(), t.get_device());
+  copy.copy_(t, /*non_blocking=*/true);
+  t = std::move(copy);
+}
+
 PyObject* fail(const char* fn, sq_status rc) {
   PyObject* e = PyObject_CallFunction(g_error_class, "si", fn, static_cast<int>(rc));
   if (e) {
@@ -121,8 +132,8 @@ PyObject* add_rmsnorm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) return nullptr;
   return guarded([&]() -> PyObject* {
     const char* fn = fp8 ? "sq_add_rmsnorm_quant_fp8" : "sq_add_rmsnorm_quant";
-    const at::Tensor &h = tensor(a[0], fn, "h"), &res = tensor(a[1], fn, "residual"),
-                     &gamma = tensor(a[2], fn, "gamma");
+    const at::Tensor &h = tensor(a[0], fn, "h"), &res = tensor(a[1], fn, "residual");
+    at::Tensor gamma = tensor(a[2], fn, "gamma");
     const int dev = device_of(fn, "h", h, 2);
     const int64_t M = h.size(0), K = h.size(1);
     fits(fn, "h", h, dev, at::kBFloat16, {M, K});
@@ -141,6 +152,7 @@ PyObject* add_rmsnorm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
       sc = make_scales(M, K, !fp8 && group != 128, dev);
       r = make({M}, at::kFloat, dev);
       c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+      align(gamma);
       rc = fp8 ? sq_add_rmsnorm_quant_fp8(h.data_ptr(), res.data_ptr(), static_cast<float*>(gamma.data_ptr()),
                                           static_cast<float>(eps), out.data_ptr(),
                                           static_cast<uint8_t*>(q.data_ptr()), static_cast<float*>(sc.data_ptr()),
@@ -175,19 +187,19 @@ PyObject* silu_mul_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = device_of(fn, "gate_up", gu, 2);
     const int64_t T = gu.size(0), K = gu.size(1) / 2;
     fits(fn, "gate_up", gu, dev, at::kBFloat16, {T, 2 * K});
-    float* inv = nullptr;
+    at::Tensor inv_s, q, sc;
     if (a[1] != Py_None) {
-      const at::Tensor& t = tensor(a[1], fn, "inv_s");
-      fits(fn, "inv_s", t, dev, at::kFloat, {K});
-      inv = static_cast<float*>(t.data_ptr());
+      inv_s = tensor(a[1], fn, "inv_s");
+      fits(fn, "inv_s", inv_s, dev, at::kFloat, {K});
     }
-    at::Tensor q, sc;
     sq_status rc;
     {
       Unlocked unlocked;
       q = make({T, K}, fp8 ? at::kByte : at::kChar, dev);
       sc = make_scales(T, K, !fp8 && group != 128, dev);
       c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+      if (inv_s.defined()) align(inv_s);
+      const float* inv = inv_s.defined() ? static_cast<const float*>(inv_s.data_ptr()) : nullptr;
       rc = fp8 ? sq_silu_mul_quant_fp8(gu.data_ptr(), inv, static_cast<uint8_t*>(q.data_ptr()),
                                        static_cast<float*>(sc.data_ptr()), T, K, stream_of(dev))
                : sq_silu_mul_quant(gu.data_ptr(), inv, group, static_cast<int8_t*>(q.data_ptr()),
@@ -205,9 +217,8 @@ PyObject* grouped_mm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) return nullptr;
   return guarded([&]() -> PyObject* {
     const char* fn = fp8 ? "fp8_block_grouped_mm" : "w8a8_grouped_mm";
-    const at::Tensor &qa = tensor(a[0], fn, "q_a"), &sa = tensor(a[1], fn, "s_a"),
-                     &qw = tensor(a[2], fn, "q_w"), &sw = tensor(a[3], fn, "s_w"),
-                     &off = tensor(a[4], fn, "offsets");
+    const at::Tensor &qa = tensor(a[0], fn, "q_a"), &qw = tensor(a[2], fn, "q_w");
+    at::Tensor sa = tensor(a[1], fn, "s_a"), sw = tensor(a[3], fn, "s_w"), off = tensor(a[4], fn, "offsets"), row;
     const int dev = device_of(fn, "q_a", qa, 2);
     device_of(fn, "q_w", qw, 3);
     const int64_t M = qa.size(0), K = qa.size(1), E = qw.size(0), N = qw.size(1);
@@ -220,25 +231,26 @@ PyObject* grouped_mm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else fits(fn, "s_w", sw, dev, at::kFloat, {E, N});
     fits(fn, "offsets", off, dev, at::kInt, {E + 1});
     int64_t T = M;
-    const int32_t* rows = nullptr;
     if (a[5] != Py_None) {
-      const at::Tensor& r = tensor(a[5], fn, "rows");
-      T = r.numel();
-      fits(fn, "rows", r, dev, at::kInt, {T});
-      rows = static_cast<const int32_t*>(r.data_ptr());
+      row = tensor(a[5], fn, "rows");
+      T = row.numel();
+      fits(fn, "rows", row, dev, at::kInt, {T});
     }
     at::Tensor y;
     if (a[6] != Py_None) {
       y = tensor(a[6], fn, "out");
       fits(fn, "out", y, dev, at::kBFloat16, {T, N});
     }
-    const float *psa = static_cast<const float*>(sa.data_ptr()), *psw = static_cast<const float*>(sw.data_ptr());
-    const int32_t* poff = static_cast<const int32_t*>(off.data_ptr());
     sq_status rc;
     {
       Unlocked unlocked;
       if (!y.defined()) y = make({T, N}, at::kBFloat16, dev);
       c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+      for (at::Tensor* t : {&sa, &sw, &off}) align(*t);
+      if (row.defined()) align(row);
+      const float *psa = static_cast<const float*>(sa.data_ptr()), *psw = static_cast<const float*>(sw.data_ptr());
+      const int32_t *poff = static_cast<const int32_t*>(off.data_ptr()),
+                    *rows = row.defined() ? static_cast<const int32_t*>(row.data_ptr()) : nullptr;
       rc = fp8 ? fp8_block_grouped_mm(static_cast<const uint8_t*>(qa.data_ptr()), psa, rows,
                                       static_cast<const uint8_t*>(qw.data_ptr()), psw, poff, y.data_ptr(), T, M, E,
                                       N, K, stream_of(dev))
