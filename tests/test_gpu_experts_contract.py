@@ -282,3 +282,19 @@ def test_factors_that_start_anywhere(fmt):
         got += call_silu(h, shifted(gamma[:384], by).requires_grad_(), fmt)
         assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, (*want, *act)))
     sq.check_device_error()
+
+
+@pytest.mark.parametrize("kind", ["i8", "fp8"])
+def test_an_output_over_an_input_is_refused(kind):
+    q_a, s_a, q_w, s_w, off, _ = cuda(*(i8_case if kind == "i8" else fp8_case)([40, 24], 128, 256, False, 215))
+    mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+    kept = q_a.clone()
+    with pytest.raises(sq.SqError) as e:
+        mm(q_a, s_a, q_w, s_w, off, out=q_a.view(torch.bfloat16))
+    assert e.value.code == 2 and torch.equal(q_a, kept)
+    h, gamma = torch.randn(64, 256, device="cuda").bfloat16(), torch.ones(256, device="cuda")
+    big = torch.zeros(65, 256, dtype=torch.bfloat16, device="cuda")
+    big[1:] = h
+    with pytest.raises(sq.SqError) as e:
+        sq.add_rmsnorm_quant(big[1:], h, gamma, EPS, residual_out=big[:-1])
+    assert e.value.code == 2

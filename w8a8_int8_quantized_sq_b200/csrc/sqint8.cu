@@ -745,10 +745,15 @@ sq_status row_quant(int fmt, const RowQuantArgs& a, cudaStream_t st) {
   return row_quant<OP, RQ_I8_ROW>(a, st);
 }
 
-// Whether [p, p + n) and [q, q + m) share a byte.
-bool overlaps(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
+// Memory that a call reads or writes, and whether two share a byte.  An output over an
+// input would be written by some rows before others have read it: refused, not answered.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlaps(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.bytes && y.bytes && a < b + y.bytes && b < a + x.bytes;
 }
 
 sq_status add_rmsnorm_quant(const void* h, const void* residual, const float* gamma, float eps,
@@ -763,10 +768,17 @@ sq_status add_rmsnorm_quant(const void* h, const void* residual, const float* ga
       !aligned16(q) || !aligned16(scales))
     return SQ_ERR_ALIGN;
   // in place means the same buffer: shifted, one row's sums would be read as another's inputs
-  const size_t bytes = static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
-  if ((residual_out != h && overlaps(residual_out, bytes, h, bytes)) ||
-      (residual_out != residual && overlaps(residual_out, bytes, residual, bytes)))
-    return SQ_ERR_SHAPE;
+  const size_t n = static_cast<size_t>(M) * static_cast<size_t>(K);
+  const size_t nsc = fmt == RQ_I8_ROW ? static_cast<size_t>(M) : n / 128;
+  const Span in[] = {{h, 2 * n}, {residual, 2 * n}, {gamma, static_cast<size_t>(K) * 4}};
+  const Span out[] = {{residual_out, 2 * n}, {q, n}, {scales, 4 * nsc},
+                      {inv_rms, inv_rms ? static_cast<size_t>(M) * 4 : 0}};
+  for (const Span& o : out)
+    for (const Span& i : in)
+      if (overlaps(o, i) && !(o.p == residual_out && i.p == o.p && i.bytes == o.bytes)) return SQ_ERR_SHAPE;
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i], out[j])) return SQ_ERR_SHAPE;
   RowQuantArgs a{};
   a.a = static_cast<const __nv_bfloat16*>(h);
   a.b = static_cast<const __nv_bfloat16*>(residual);
@@ -791,6 +803,11 @@ sq_status silu_mul_quant(const void* gate_up, const float* inv_smooth, int fmt, 
   if (!aligned16(gate_up) || !aligned16(q) || !aligned16(scales) ||
       (inv_smooth && !aligned16(inv_smooth)))
     return SQ_ERR_ALIGN;
+  const size_t n = static_cast<size_t>(M) * static_cast<size_t>(K);
+  const Span x{gate_up, 4 * n}, inv{inv_smooth, inv_smooth ? static_cast<size_t>(K) * 4 : 0}, codes{q, n},
+      sc{scales, 4 * (fmt == RQ_I8_ROW ? static_cast<size_t>(M) : n / 128)};
+  if (overlaps(codes, x) || overlaps(codes, inv) || overlaps(sc, x) || overlaps(sc, inv) || overlaps(codes, sc))
+    return SQ_ERR_SHAPE;
   RowQuantArgs a{};
   a.a = static_cast<const __nv_bfloat16*>(gate_up);
   a.vec = inv_smooth;
@@ -904,6 +921,12 @@ sq_status grouped_mm(bool f8, const void* q_a, const float* s_a, const int32_t* 
   if (!aligned16(q_a) || !aligned16(s_a) || !aligned16(q_w) || !aligned16(s_w) ||
       !aligned16(offsets) || !aligned16(y) || (rows && !aligned16(rows)))
     return SQ_ERR_ALIGN;
+  const auto z = [](int64_t n) { return static_cast<size_t>(n); };
+  const Span in[] = {{q_a, z(M) * z(K)}, {s_a, z(M) * (f8 ? z(K / 128) : 1) * 4}, {rows, rows ? z(T) * 4 : 0},
+                     {q_w, z(E) * z(N) * z(K)}, {s_w, z(E) * (f8 ? z(N / 128) * z(K / 128) : z(N)) * 4},
+                     {offsets, z(E + 1) * 4}};
+  for (const Span& i : in)
+    if (overlaps({y, z(T) * z(N) * 2}, i)) return SQ_ERR_SHAPE;
   GroupedArgs g{};
   g.offsets = offsets;
   g.rows = rows;
