@@ -236,7 +236,7 @@ sq_status fp8_block_mm(const uint8_t* q_a, const float* s_a, const uint8_t* q_w,
  * h, residual, residual_out BF16 [M,K]; residual_out may be the residual or h
  * itself (in place).  Otherwise an output that overlaps an input or another output
  * is refused (SQ_ERR_SHAPE), here and in the calls below.
- * inv_rms (fp32 [M], may be NULL) receives r.  eps > 0; K <= 24576.  Where a row
+ * inv_rms (fp32 [M], 4-byte aligned, may be NULL) receives r.  eps > 0; K <= 24576.  Where a row
  * (group == 128: 128 columns of it) has a v that is NaN or infinite, its scale is
  * NaN or infinite, so that products with it are too, and its codes are
  * unspecified; a NaN in x is in every v of its row.  The other rows are not

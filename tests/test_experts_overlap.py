@@ -1,6 +1,6 @@
-"""The expert entry points refuse an output that overlaps an input or another output (status 2).
-Checked before any CUDA call; the addresses are never dereferenced, and every call here is one
-to refuse."""
+"""The expert entry points refuse an output that overlaps an input or another output (status 2),
+and a 1/rms output that no float can be stored to (3).  Checked before any CUDA call; the
+addresses are never dereferenced, and every call here is one to refuse."""
 from __future__ import annotations
 
 import ctypes
@@ -63,6 +63,8 @@ def test_norm(lib, group):
         p = [at(j) for j in range(7)]
         p[o] = where
         assert call(p) == 2, (o, i, hex(where.value))
+    for byte in (1, 2, 3):
+        assert call([at(j) for j in range(6)] + [at(6, byte)]) == 3
 
 
 @pytest.mark.parametrize("group", [0, 128, "fp8"])

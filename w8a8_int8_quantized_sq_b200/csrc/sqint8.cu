@@ -767,6 +767,7 @@ sq_status add_rmsnorm_quant(const void* h, const void* residual, const float* ga
   if (!aligned16(h) || !aligned16(residual) || !aligned16(gamma) || !aligned16(residual_out) ||
       !aligned16(q) || !aligned16(scales))
     return SQ_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(inv_rms) % sizeof(float)) return SQ_ERR_ALIGN;
   // in place means the same buffer: shifted, one row's sums would be read as another's inputs
   const size_t n = static_cast<size_t>(M) * static_cast<size_t>(K);
   const size_t nsc = fmt == RQ_I8_ROW ? static_cast<size_t>(M) : n / 128;
