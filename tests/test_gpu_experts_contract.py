@@ -298,3 +298,32 @@ def test_an_output_over_an_input_is_refused(kind):
     with pytest.raises(sq.SqError) as e:
         sq.add_rmsnorm_quant(big[1:], h, gamma, EPS, residual_out=big[:-1])
     assert e.value.code == 2
+
+
+def test_fp8_rows_of_a_call_of_32_are_those_of_a_call_of_31():
+    """Calls of 31 and of 32 rows over 4 experts make the same tiles, so they share K among as
+    many pairs, and their common rows have the same bits."""
+    for counts in ([8, 8, 8, 8], [1, 29, 1, 1], [32]):
+        c = fp8_case(counts, 2048, 5120, False, 207)
+        q_a, s_a, q_w, s_w, off = cuda(*c[:5])
+        y = sq.fp8_block_grouped_mm(q_a, s_a, q_w, s_w, off)
+        less = sq.fp8_block_grouped_mm(q_a[:31].contiguous(), s_a[:31].contiguous(), q_w, s_w,
+                                       off.clamp(max=31))
+        assert torch.equal(y[:31], less), int((y[:31] != less).sum())
+        check_fp8(y, c, counts)
+
+
+@pytest.mark.parametrize("kind", ["i8", "fp8"])
+def test_grouped_tiles_fill_their_bound(kind):
+    """The most token tiles that T rows over E experts can make: one row in every expert but
+    one, which has the rest.  Row counts around the tile heights."""
+    for T in (31, 32, 33, 127, 128, 129, 255, 256, 257, 258, 512, 513):
+        for E in (1, 2, 5):
+            c = (i8_case if kind == "i8" else fp8_case)([1] * (E - 1) + [T - E + 1], 128, 256, False, 216)
+            mm = sq.w8a8_grouped_mm if kind == "i8" else sq.fp8_block_grouped_mm
+            y = mm(*cuda(*c[:5]))
+            if kind == "i8":
+                assert_bits(y, i8_reference(*c, torch.zeros(T, 128, dtype=torch.bfloat16)), (T, E))
+            else:
+                check_fp8(y, c, (T, E))
+    sq.check_device_error()

@@ -84,13 +84,22 @@ struct GroupedMaps {
 // a deeper ring does not change that): there a tile's K is split over the 2 to 4 CTA
 // pairs of one cluster.  The other pairs' partial sums meet in the first's shared
 // memory and are added in the order of K, so the answer does not depend on timing.
-// Measured with N = 2048, us, on the pairs given:
-//   1 row, 8 tiles, on 4, 2 and 1:   K = 2048: INT8 8.1, 8.2, 8.9; FP8 8.6, 8.6, 9.6
-//                                    K = 5120: INT8 9.4, 11.1, 14.7; FP8 10.1, 11.8, 15.6
-//   2 rows, 16 tiles, on 3, 2 and 1: K = 2048: INT8 8.2, 8.3, 8.9; FP8 9.0, 8.8, 9.7
-//                                    K = 5120: INT8 10.1, 11.2, 14.8; FP8 11.1, 11.9, 15.7
-//   4 rows, 32 tiles, on 2 and 1:    K = 2048: INT8 9.1, 9.0; FP8 10.0, 9.7
-//                                    K = 5120: INT8 13.6, 15.4; FP8 14.4, 16.3
+// Measured with one row per expert, N = 2048 (8 tiles per expert), us (32 rows in all: up to
+// 0.5 us more with two pairs and more, the rest alike), on 1, 2, 3 and 4 pairs per tile:
+//   tiles, K      INT8                       FP8
+//    8, 1024       5.6   6.1   6.1   6.6      6.1   6.5   6.5   7.0
+//    8, 2048       8.0   7.7   7.3   7.8      8.6   8.0   7.6   7.9
+//    8, 5120      13.7  10.5   9.2   9.3     14.5  11.1   9.8   9.8
+//   16, 1536       7.3   7.5   7.8            7.9   8.0   8.1
+//   16, 2048       8.2   8.0   8.2            8.9   8.4   8.6
+//   16, 5120      13.8  10.7  10.3           14.6  11.5  10.9
+//   24, 2048       8.3   8.7                  9.0   9.2
+//   24, 2560       9.3   9.3                 10.0   9.9
+//   24, 3584      11.1  10.3                 11.9  11.0
+//   32, 2048       8.5   9.5                  9.2  10.0
+//   32, 2560       9.4  10.1                 10.1  10.7
+//   32, 3584      11.3  11.4                 12.1  11.9
+//   32, 5120      14.2  13.3                 15.0  13.8
 // With more tiles than resident clusters the 32-token tiles on one pair are no faster
 // than the wide ones (8 to 64 rows: 0 to 4 % slower), so those run the wide ones.
 template <bool F8_, int BT_>

@@ -854,10 +854,15 @@ int grouped_clusters(int split) {
   return mc;
 }
 
-// Most tiles the offsets can give: each group of rows ends in at most one partial tile.
+// Most tiles the offsets can give: a group of r rows has 1 + (r - 1) / BT token tiles, so n
+// groups of T rows together have at most n + (T - n) / BT, the more the larger n is.  (32 rows
+// are one tile per group, like 31.  A bound of n + T / BT left them on fewer pairs than the
+// rule below asks for: 32 rows over 4 experts, K = 5120, N = 2048, INT8 14.4 us, FP8 15.2,
+// against 13.1 and 13.6.)
 template <class Cfg>
 int64_t grouped_tiles(const GroupedArgs& g) {
-  return static_cast<int64_t>((g.T < g.E ? g.T : g.E) + g.T / Cfg::BT) * g.tiles_n;
+  const int n = g.T < g.E ? g.T : g.E;
+  return static_cast<int64_t>(n + (g.T - n) / Cfg::BT) * g.tiles_n;
 }
 
 // On clusters of g.split pairs, at most mc of them.
@@ -883,19 +888,20 @@ sq_status launch_grouped(const void* q_a, const void* q_w, const GroupedArgs& g,
                           Cfg::THREADS, Cfg::smem_bytes(), st, 2 * g.split, tw, tx, g);
 }
 
-// A tile's K over 4, 3 or 2 pairs where every tile can have a resident cluster of its own
-// and a pair keeps eight K blocks (of two pairs: two) or more, with fewer of which a larger
-// cluster gains nothing; else one pair per tile.  (Both measured, with
-// 32-token tiles on one pair too, beside the kernel.)
+// A tile's K over 4, 3 or 2 pairs where every tile can have a resident cluster of its own, a
+// pair keeps eight K blocks or more, and there are K blocks for five sixths of the tiles (the
+// more tiles, the less of the device a split can put to use: 24 gain from 20 blocks on, 32
+// from 28); else one pair per tile.  (All sides measured beside the kernel.)
 template <bool F8>
 sq_status launch_grouped(const void* q_a, const void* q_w, GroupedArgs g, cudaStream_t st) {
   using Narrow = GroupedCfg<F8, 32>;
   using Wide = GroupedCfg<F8, F8 ? 128 : 256>;
   if (g.T <= Narrow::BT) {
     for (g.split = 4; g.split > 1; --g.split) {
-      if (g.kb_total < (g.split > 2 ? 8 : 2) * g.split) continue;
+      const int64_t tiles = grouped_tiles<Narrow>(g);
+      if (g.kb_total < 8 * g.split || 6 * g.kb_total < 5 * tiles) continue;
       const int mc = grouped_clusters<Narrow>(g.split);  // 0 where no cluster of this size fits
-      if (grouped_tiles<Narrow>(g) <= mc) return launch_grouped<Narrow>(q_a, q_w, g, mc, st);
+      if (tiles <= mc) return launch_grouped<Narrow>(q_a, q_w, g, mc, st);
     }
   }
   g.split = 1;
