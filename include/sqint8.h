@@ -383,12 +383,15 @@ sq_status sq_describe_plan(int op, int64_t M, int64_t N, int64_t K, int sms,
 sq_status sq_mma_peak(int kind, int iters, void* stream, double* ops_per_launch);
 
 /* Self-test of the timeout path (the pages have no counterpart).  Launches on
- * `stream` one thread that waits, with a limit of limit_cycles SM clock
- * cycles (0 < limit_cycles <= 4e9), on a barrier that nothing arrives on.
- * The wait gives up exactly as a GEMM role's wait does: it raises the kernel's
+ * `stream` one thread, and after it one warp, that wait, each with a limit of
+ * limit_cycles SM clock cycles (0 < limit_cycles <= 4e9), on a barrier that nothing
+ * arrives on: the thread as the GEMM roles wait, the warp as the grouped products'
+ * accumulator waits.  Each gives up exactly as there: it raises the kernel's
  * abort flag and latches the device error word, so sq_check_device_error
- * then returns SQ_ERR_TIMEOUT.  gave_up (device int) receives 1 when the
- * wait gave up through its own limit.  Nothing else runs in that kernel. */
+ * then returns SQ_ERR_TIMEOUT; a last wait ends at once because the flag is up.
+ * gave_up (device int) receives 1 when all that happened, else 0 (a wait passed), 2
+ * (the flag was not raised), 3 (the word was not latched) or 4 (the flag was not
+ * heeded).  Nothing else runs in that kernel. */
 sq_status sq_selftest_wait_timeout(int64_t limit_cycles, int* gave_up, void* stream);
 
 /* Diagnostics ------------------------------------------------------------ */

@@ -327,3 +327,26 @@ def test_grouped_tiles_fill_their_bound(kind):
             else:
                 check_fp8(y, c, (T, E))
     sq.check_device_error()
+
+
+def test_the_accumulator_wait_gives_up_too():
+    """The self-test runs one wait of each kind to its limit (two limits' time in all), and the
+    expert operators answer as before once the error word is cleared."""
+    c = i8_case([3, 0, 29, 200], 256, 640, True, 217)
+    args, rows = cuda(*c[:5]), cuda(c[5])[0]
+    want = sq.w8a8_grouped_mm(*args, rows=rows)
+    sq.check_device_error()
+    limit = 100_000_000
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    assert sq.selftest_wait_timeout(limit) == 1
+    end.record()
+    end.synchronize()
+    # a clock of at most 2 GHz; one limit alone would be over in 50 ms at 2 GHz
+    took, clock = start.elapsed_time(end) * 1e-3, 2.0e9
+    assert took >= 2 * limit / clock, took
+    with pytest.raises(sq.SqError) as e:
+        sq.check_device_error(reset=True)
+    assert e.value.code == 6
+    assert torch.equal(sq.w8a8_grouped_mm(*args, rows=rows), want)
+    sq.check_device_error()

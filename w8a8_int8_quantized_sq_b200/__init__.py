@@ -474,7 +474,7 @@ def mma_peak(kind: int = PEAK_I8, iters: int = 8192, launches: int = 4, device=N
 
 def selftest_wait_timeout(limit_cycles: int = 2_000_000, device=None) -> int:
     """Run the timeout self-test kernel (sq_selftest_wait_timeout) and return
-    its gave_up flag (1: the wait gave up through its own limit).  The device
+    its gave_up flag (1: every wait gave up through its own limit).  The device
     error word is left set: check_device_error() then raises SQ_ERR_TIMEOUT."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     flag = torch.full((1,), -1, dtype=torch.int32, device=dev)

@@ -145,50 +145,6 @@ struct GroupedCfg {
   static_assert(!F8 || BT <= 128, "FP8 epilogue: two groups of at most 64 columns");
 };
 
-// mbarrier wait without a suspend-time hint, bounded like wait_bounded, the same answer
-// in every lane: for the accumulators' round trip (MMA, commit, epilogue, release,
-// MMA), where waking from the hint's suspension showed (8198 rows, FP8 122 us against
-// 120; 32768 rows, INT8 123 against 121.5).  The other roles keep the hint: their
-// polling would take issue slots.
-__device__ __forceinline__ bool prompt_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const uint32_t a = smem_u32(bar);
-  bool ok = prompt_try_wait(a, parity);
-  if (!ok) {
-    const long long t0 = sm_cycles();
-    for (;;) {
-#pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = prompt_try_wait(a, parity);
-      if (ok || *abort_flag) break;
-      if (sm_cycles() - t0 > kWaitLimitCycles) {
-        *abort_flag = 1;
-        atomicOr(&g_error_word, kErrTimeout);
-        break;
-      }
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
-}
-// Both phases complete.  The two polls overlap: the MMA warp's turn (polls, four MMAs,
-// commits) has to stay below the MMAs' own time, and two waits one after the other
-// did not.
-__device__ __forceinline__ bool prompt_wait2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1,
-                                             uint32_t parity1, volatile int* abort_flag) {
-  const bool a = prompt_try_wait(smem_u32(bar0), parity0), b = prompt_try_wait(smem_u32(bar1), parity1);
-  if (__all_sync(0xffffffffu, a && b)) return true;
-  return prompt_wait(bar0, parity0, abort_flag) && prompt_wait(bar1, parity1, abort_flag);
-}
-
 // Asynchronous load of 32 columns of 16 tensor-memory lanes (taddr: lane 0 or 16 of
 // the warp's quadrant) as matrix fragments: lane l gets, for columns 8 i + 2 (l % 4)
 // and the next, rows l / 4 (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]).

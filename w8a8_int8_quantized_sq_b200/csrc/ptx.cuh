@@ -90,19 +90,95 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
   }
 }
 
-// Self-test of the timeout path: one thread waits on an mbarrier that nothing
-// arrives on, with a short limit; the wait gives up, raises the abort flag
-// and latches the device error word exactly as a GEMM role's wait would.  No
-// copy, MMA or tensor memory is involved, so the kernel simply returns.
+// mbarrier wait without a suspend-time hint, bounded like wait_bounded, the same answer
+// in every lane: for the accumulators' round trip of the grouped products (MMA, commit,
+// epilogue, release, MMA), where waking from the hint's suspension showed (8198 rows, FP8 122 us against
+// 120; 32768 rows, INT8 123 against 121.5).  The other roles keep the hint: their
+// polling would take issue slots.
+__device__ __forceinline__ bool prompt_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                            long long limit = kWaitLimitCycles) {
+  const uint32_t a = smem_u32(bar);
+  bool ok = prompt_try_wait(a, parity);
+  if (!ok) {
+    const long long t0 = sm_cycles();
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = prompt_try_wait(a, parity);
+      if (ok || *abort_flag) break;
+      if (sm_cycles() - t0 > limit) {
+        *abort_flag = 1;
+        atomicOr(&g_error_word, kErrTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+// Both phases complete.  The two polls overlap: the MMA warp's turn (polls, four MMAs,
+// commits) has to stay below the MMAs' own time, and two waits one after the other
+// did not.
+__device__ __forceinline__ bool prompt_wait2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1,
+                                             uint32_t parity1, volatile int* abort_flag) {
+  const bool a = prompt_try_wait(smem_u32(bar0), parity0), b = prompt_try_wait(smem_u32(bar1), parity1);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return prompt_wait(bar0, parity0, abort_flag) && prompt_wait(bar1, parity1, abort_flag);
+}
+
+// Self-test of the timeout path: one thread, then a whole warp, waits on an mbarrier that
+// nothing arrives on, with a short limit; each wait gives up, raises the abort flag and
+// latches the device error word exactly as a GEMM role's wait would; a last one ends at
+// once because the flag is up.  No copy, MMA or tensor memory is involved, so the kernel
+// simply returns.  *gave_up: 1, or what did not happen: 0 a wait passed, 2 the flag was not
+// raised, 3 the word was not latched, 4 the flag was not heeded.
 __global__ void wait_timeout_selftest_kernel(long long limit_cycles, int* gave_up) {
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
-  if (threadIdx.x == 0) {
+  const int lane = threadIdx.x;
+  int answer = 1;
+  auto expect = [&](bool holds, int otherwise) {
+    if (!holds && answer == 1) answer = otherwise;
+  };
+  unsigned int before = 0;
+  if (lane == 0) {
     mbar_init(&bar, 1);
-    abort_flag = 0;
     fence_mbar_init();
-    const bool ok = wait_bounded(&bar, 0, &abort_flag, limit_cycles);
-    *gave_up = ok ? 0 : (abort_flag ? 1 : 2);
+    before = atomicExch(&g_error_word, 0u);  // put back below
+  }
+  for (int kind = 0; kind < 2; ++kind) {
+    if (lane == 0) abort_flag = 0;
+    __syncwarp();
+    bool ok = false;
+    if (kind == 1) ok = prompt_wait(&bar, 0, &abort_flag, limit_cycles);
+    else if (lane == 0) ok = wait_bounded(&bar, 0, &abort_flag, limit_cycles);
+    expect(!__any_sync(0xffffffffu, ok), 0);
+    if (lane == 0) {
+      expect(*static_cast<volatile int*>(&abort_flag) == 1, 2);
+      const unsigned int word = atomicExch(&g_error_word, 0u);
+      expect((word & kErrTimeout) != 0, 3);
+      before |= word;
+    }
+    __syncwarp();
+  }
+  if (lane == 0) abort_flag = 1;
+  __syncwarp();
+  const long long t0 = sm_cycles();
+  const bool ok = prompt_wait2(&bar, 0, &bar, 0, &abort_flag);
+  expect(!__any_sync(0xffffffffu, ok), 0);
+  expect(sm_cycles() - t0 < kWaitLimitCycles / 2, 4);
+  if (lane == 0) {
+    atomicOr(&g_error_word, before);
+    *gave_up = answer;
   }
 }
 
