@@ -336,8 +336,8 @@ sq_status sq_quant_weight(const void* w_bf16, const float* smooth, int8_t* q_w, 
  * kernel before it on the stream is still running: it requests its WEIGHT
  * tiles (q_w) at once and reads everything else (activations, scales,
  * workspace, output) only after that kernel has completed.  Enable it only
- * if no kernel that directly precedes such a call on its stream writes that
- * call's q_w.  enable == 0 (the default): every launch waits for the
+ * if no kernel that directly precedes such a call on its stream, or that only
+ * calls under this policy separate from it, writes that call's q_w.  enable == 0 (the default): every launch waits for the
  * preceding work as usual.  sq_w8a8_linear always overlaps its GEMM with its
  * own quantisation kernel.  Always returns SQ_OK. */
 sq_status sq_set_overlap(int enable);

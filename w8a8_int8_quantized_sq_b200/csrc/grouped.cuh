@@ -35,18 +35,21 @@
 // What bounds it, measured on one B200 (INT8 codes of normal values unless said):
 //   INT8, 8 experts x 1024 rows, N = 8192: K = 5120 225-232 us (3000 TOPS; 4030 with zero
 //     codes, so the power limit, not the pipeline), K = 2048 98-102 us (2750 TOPS).
-//   INT8, 32768 rows over 64 experts, K = N = 2048: 122-126 us, gathered 124-128 us (104 us
-//     with zero codes).  Token tiles that are not full and the uneven last wave cost the rest.
-//   INT8, 128 rows over 64 experts, K = 2048, N = 1536: 33.4 us, 5.3 TB/s in all.
+//   INT8, 32768 rows over 64 experts, K = N = 2048: 122-126 us, gathered 124-130 us (104 us
+//     with zero codes; 152 us in a long sequence, at lower clocks).  Token tiles that are not
+//     full and the uneven last wave cost the rest.
+//   INT8, 128 rows over 53 of 64 experts, K = 2048, N = 1536: 33.6 us, 5.0 TB/s in all.
 //   FP8, 8198 rows over 8 experts, K = 5120, N = 2048: 119 us, 1440 TOPS (127 us
-//     gathered); the loads and MMAs alone take 87 us.  The epilogue's own chain per K block
-//     (tensor-memory reads of 64 bytes per clock and SM quadrant, releases, fused
-//     multiply-adds) bounds it.  With branches on the warp's chunks inside the K loop and
+//     gathered, 148 us in a long sequence).  Of the gathered call's 127, with the
+//     promotion's fused multiply-adds left out 105 us, with the tensor-memory reads too 102:
+//     the hand-offs between loads, MMAs and releases.  L2 is at 24 % of its rate to the
+//     SMs.  With branches on the warp's chunks inside the K loop and
 //     both chunks read before either was added it took 139 us.
-//     Slower variants: lanes as channels with broadcast scales (220 us), 16 epilogue
-//     warps of 32 columns (143 us but decode 6 % slower), 192- and 256-token tiles with two
-//     accumulators (240-400 us).
-//   FP8, 222 rows over 64 experts, K = 1408, N = 2048: 33.1 us, 5.5 TB/s in all.
+//     Slower variants, each against the kernel of its time (138-146 us): lanes as channels
+//     with broadcast scales (220 us), 192- and 256-token tiles with two accumulators
+//     (240-400 us); 16 epilogue warps of 32 columns gained nothing (143 us, decode 6 % slower)
+//     and were not measured again on the present K loop.
+//   FP8, 222 rows over 60 of 64 experts, K = 1408, N = 2048: 33.2 us, 5.2 TB/s in all.
 //   Token rows copied by cp.async threads instead of TMA ran 2-3 times slower (the
 //   proxy fences wait for every copy in flight).
 #pragma once
